@@ -95,6 +95,9 @@ typedef struct loom_launch_config {
  *   "packed_dot"      (outputs, count, streams)
  *   "sum_guarded_rows" (count)
  *   "routed_combine"  (tokens, routes, hidden)
+ *   "quantize_rows"   (rows, cols)
+ *   "i8_matmul", "i8_gated_projection" (rows, k, tokens)
+ *   "i8_gated_projection_backward" (rows, k, tokens): its first kernel
  * lookup: LOOM_ERR_NULL if a pointer is NULL, LOOM_ERR_UNKNOWN_EXPORT if no
  * kernel has that name.  The token stays valid for the life of the process. */
 int loom_launch_config_lookup(const char *export_name, uint32_t *token);
@@ -318,6 +321,99 @@ int loom_sum_guarded_rows(const float *values, int64_t rows_alloc, int64_t count
  * ------------------------------------------------------------------------ */
 int loom_routed_combine(const int32_t *ids, const float *weights, const float *payload, int64_t num_rows,
                         int64_t tokens, int64_t routes, int64_t hidden, float *out, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * The int8 feed-forward operators.  Activations are quantised by token       *
+ * (loom_quantize_rows), multiplied by int8 weights with one scale a channel, *
+ * for any number of tokens, and every result is in token order.             *
+ * ------------------------------------------------------------------------ */
+
+/* Element types of activations, outputs and gradients. */
+typedef enum loom_type { LOOM_F32 = 0, LOOM_F16 = 1, LOOM_BF16 = 2 } loom_type;
+
+/* Activations of a gated unit: g / (1 + exp(-g)); g Phi(g) (erf); its tanh
+ * form 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))); max(g, 0). */
+typedef enum loom_activation { LOOM_SILU = 0, LOOM_GELU = 1, LOOM_GELU_TANH = 2, LOOM_RELU = 3 } loom_activation;
+
+/* ------------------------------------------------------------------------ *
+ * Symmetric int8 quantisation of rows (tokens).  With a = max_c |x[r][c]|:  *
+ *     scale[r] = a / 127,   q[r][c] = rint(x[r][c] * (127 / a))             *
+ * each quotient and product one f32 rounding, rint to even.  A row with     *
+ * a < 2^-119 (an empty or zero row too) gives zeros and scale 0; a row that *
+ * holds an infinity or a NaN gives zeros and scale NaN, which makes every   *
+ * product of that row NaN.                                                  *
+ *   x          : type[rows], rows row_stride elements apart, device,        *
+ *                aligned to its element                                     *
+ *   rows, cols : 0 .. 2^31 - 1; cols % 4 == 0 (LOOM_ERR_SHAPE)              *
+ *   row_stride : >= cols (LOOM_ERR_SHAPE); 4 * rows * row_stride must fit   *
+ *                in an int64 (LOOM_ERR_RANGE)                               *
+ *   q          : int32[rows][cols/4] packed int8, device                    *
+ *   scale      : f32[rows], device                                          *
+ * ------------------------------------------------------------------------ */
+int loom_quantize_rows(const void *x, int type, int64_t rows, int64_t cols, int64_t row_stride, int32_t *q,
+                       float *scale, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Int8 matrix product with a scale for each token and each channel.         *
+ *     acc[t][n] = sum_{i < k} w[n][i] * x[t][i]            (exact, int32)   *
+ *     out[t][n] = (f32(acc[t][n]) * w_scale[n]) * x_scale[t] + bias[n]      *
+ * each operation one f32 rounding, the result rounded once to the output    *
+ * type; a NULL x_scale or bias leaves its operation out.                    *
+ *   w          : int32[rows][k/4] packed int8 weights, device               *
+ *   w_scale    : f32[rows], device                                          *
+ *   x          : int32[tokens][k/4] packed int8 activations, device         *
+ *   x_scale    : f32[tokens], device, or NULL (= 1)                         *
+ *   bias       : f32[rows], device, or NULL (= 0)                           *
+ *   rows       : channels, 0 <= rows < 2^31                                 *
+ *   k          : k % 4 == 0 (LOOM_ERR_SHAPE), 0 <= k <= 131068              *
+ *   tokens     : 0 <= tokens < 2^31; LOOM_ERR_RANGE also when the grid      *
+ *                would reach 2^32 work-items, as loom_launch_config_invoke  *
+ *                reports for (rows, k, tokens)                              *
+ *   out        : type[tokens], rows out_stride >= rows elements apart       *
+ *                (LOOM_ERR_SHAPE), device, aligned to its element;          *
+ *                4 * tokens * out_stride must fit in an int64               *
+ * ------------------------------------------------------------------------ */
+int loom_i8_matmul(const int32_t *w, const float *w_scale, const int32_t *x, const float *x_scale, const float *bias,
+                   int64_t rows, int64_t k, int64_t tokens, void *out, int type, int64_t out_stride, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Gated projection: both products, the activation and the product of the    *
+ * two in one kernel.  With g and u the scaled products of loom_i8_matmul    *
+ * (no bias) for the two weights,                                            *
+ *     out[t][n] = act(g[t][n]) * u[t][n]                                    *
+ * in f32, rounded once to the output type.  Arguments as there, each for    *
+ * both weights; act is a loom_activation (LOOM_ERR_RANGE otherwise).        *
+ * ------------------------------------------------------------------------ */
+int loom_i8_gated_projection(const int32_t *w_gate, const float *gate_scale, const int32_t *w_up,
+                             const float *up_scale, const int32_t *x, const float *x_scale, int64_t rows, int64_t k,
+                             int64_t tokens, int act, void *out, int type, int64_t out_stride, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Gradients of the gated projection, for tuning over frozen int8 weights.   *
+ * With g, u recomputed (the same bits as the forward pass) and d = d_out,   *
+ *     dg = d * u * act'(g),   du = d * act(g)                               *
+ *     d_x[t][i] = sum_f dg[t][f] gate_scale[f] w_gate[f][i]                 *
+ *                     + du[t][f] up_scale[f] w_up[f][i]                     *
+ *     d_gate_scale[f] = sum_t dg[t][f] acc_gate[t][f] x_scale[t]            *
+ *     d_up_scale[f]   = sum_t du[t][f] acc_up[t][f] x_scale[t]              *
+ * d_x is the gradient of the dequantised activation x * x_scale, what a     *
+ * straight-through estimator passes on.  ReLU's derivative at 0 is 0.  All  *
+ * sums are f32 in a fixed order: the same bits on every call.               *
+ *   d_out        : type[tokens], rows d_stride >= rows elements apart       *
+ *   d_x          : type[tokens][k] (the type of d_out), device, or NULL     *
+ *   d_gate_scale, d_up_scale : f32[rows], device, or NULL                   *
+ *   workspace    : device memory, 16-byte aligned, of at least the bytes    *
+ *                  that loom_i8_gated_projection_backward_workspace gives   *
+ *                  for the same sizes (LOOM_ERR_RANGE); its contents after  *
+ *                  the call mean nothing                                    *
+ * With no tokens the scale gradients are 0, with no channels d_x is.        *
+ * ------------------------------------------------------------------------ */
+int loom_i8_gated_projection_backward_workspace(int64_t rows, int64_t k, int64_t tokens, int type, int64_t *bytes);
+int loom_i8_gated_projection_backward(const int32_t *w_gate, const float *gate_scale, const int32_t *w_up,
+                                      const float *up_scale, const int32_t *x, const float *x_scale, int64_t rows,
+                                      int64_t k, int64_t tokens, int act, const void *d_out, int type,
+                                      int64_t d_stride, void *d_x, float *d_gate_scale, float *d_up_scale,
+                                      void *workspace, int64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

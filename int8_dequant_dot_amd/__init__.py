@@ -41,17 +41,31 @@ _lib.loom_i8_dequant_dot.argtypes = [_p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _
 _lib.loom_packed_dot.argtypes = [_p, _p, _p, _i64, _p, _i64, _i64, _i64, _p, _p]
 _lib.loom_sum_guarded_rows.argtypes = [_p, _i64, _i64, _i64, _i64, _p, _p]
 _lib.loom_routed_combine.argtypes = [_p, _p, _p, _i64, _i64, _i64, _i64, _p, _p]
+_lib.loom_quantize_rows.argtypes = [_p, ctypes.c_int, _i64, _i64, _i64, _p, _p, _p]
+_lib.loom_i8_matmul.argtypes = [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p, ctypes.c_int, _i64, _p]
+_lib.loom_i8_gated_projection.argtypes = [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, ctypes.c_int, _p, ctypes.c_int,
+                                          _i64, _p]
+_lib.loom_i8_gated_projection_backward_workspace.argtypes = [_i64, _i64, _i64, ctypes.c_int, _p]
+_lib.loom_i8_gated_projection_backward.argtypes = [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, ctypes.c_int, _p,
+                                                   ctypes.c_int, _i64, _p, _p, _p, _p, _i64, _p]
 for _name in ("loom_launch_config_lookup", "loom_launch_config_invoke", "loom_copy_f32", "loom_row_sum_tiles",
               "loom_row_sums", "loom_segment_sums", "loom_segment_sums_noalloc", "loom_i8_dequant_dot",
               "loom_packed_dot",
-              "loom_sum_guarded_rows", "loom_routed_combine"):
+              "loom_sum_guarded_rows", "loom_routed_combine", "loom_quantize_rows", "loom_i8_matmul",
+              "loom_i8_gated_projection", "loom_i8_gated_projection_backward_workspace",
+              "loom_i8_gated_projection_backward"):
     getattr(_lib, _name).restype = ctypes.c_int
 
 # status codes (include/loom.h)
 OK, ERR_NULL, ERR_RANGE, ERR_ALIGN, ERR_SHAPE, ERR_UNKNOWN_EXPORT, ERR_TOKEN, ERR_DEVICE = 0, -1, -2, -3, -4, -5, -6, -7
 
 EXPORTS = ("copy_f32", "row_sum_tiles", "row_sums", "segment_sums", "i8_dequant_dot", "packed_dot",
-           "sum_guarded_rows", "routed_combine")
+           "sum_guarded_rows", "routed_combine", "quantize_rows", "i8_matmul", "i8_gated_projection",
+           "i8_gated_projection_backward")
+
+# loom_type and loom_activation (include/loom.h)
+_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 
 
 class LoomError(RuntimeError):
@@ -302,6 +316,150 @@ def routed_combine(ids: torch.Tensor, weights: torch.Tensor, payload: torch.Tens
     _check(_lib.loom_routed_combine(_ptr(ids), _ptr(weights), _ptr(payload), num_rows, tokens, routes, hidden,
                                     _ptr(out), stream), "routed_combine")
     return out
+
+
+# ------------------------------------------------------------------ int8 feed-forward operators
+
+def _type(dtype, name: str) -> int:
+    if dtype not in _TYPES:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {dtype}")
+    return _TYPES[dtype]
+
+
+def _act(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _rows_of(t: torch.Tensor, dtype, rows: int, cols: int, name: str, device: int) -> int:
+    """Checks a [rows][cols] matrix with unit column stride and any row stride >= cols; returns the row stride."""
+    _dev(t, dtype, name, device)
+    _require(t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols,
+             f"{name} must be [{rows}][{cols}], got {list(t.shape)}")
+    if rows == 0 or cols == 0:
+        return max(cols, 1)
+    _require(cols == 1 or t.stride(1) == 1, f"{name} must have unit column stride")
+    if rows == 1:
+        return cols
+    _require(t.stride(0) >= cols, f"{name} has overlapping rows")
+    return t.stride(0)
+
+
+def _product_operands(w, w_scale, x, x_scale, device, w_name="w", s_name="w_scale"):
+    """Checks packed weights [rows][k/4], activations [tokens][k/4] and their scales -> (rows, k, tokens, x)."""
+    _dev(w, torch.int32, w_name, device)
+    _dev(x, torch.int32, "x", device)
+    if x.dim() == 1:
+        x = x.view(1, -1)
+    _require(w.dim() == 2 and w.is_contiguous(), f"{w_name} must be a contiguous [rows][k/4] tensor")
+    _require(x.dim() == 2 and x.is_contiguous() and x.shape[1] == w.shape[1],
+             f"x must be a contiguous [tokens][k/4] tensor with the same k as {w_name}")
+    rows, kw = w.shape
+    _buffer(w_scale, torch.float32, rows, s_name, device)
+    _buffer(x_scale, torch.float32, x.shape[0], "x_scale", device, optional=True)
+    return rows, 4 * kw, x.shape[0], x
+
+
+def quantize_rows(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None):
+    """x [rows][cols] f32, f16 or bf16 with unit column stride (any row stride), cols % 4 == 0
+    -> (q int32 [rows][cols/4] packed int8, scale f32 [rows]) with x ~ q * scale, |q| <= 127."""
+    device, stream = _target(x, "x")
+    kind = _type(x.dtype, "x")
+    _require(x.dim() == 2, "x must be [rows][cols]")
+    rows, cols = x.shape
+    stride = _rows_of(x, x.dtype, rows, cols, "x", device)
+    _require(cols % 4 == 0, "x must have a multiple of 4 columns")
+    if q is None:
+        q = torch.empty(rows, cols // 4, dtype=torch.int32, device=x.device)
+    _buffer(q, torch.int32, rows * (cols // 4), "q", device)
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _buffer(scale, torch.float32, rows, "scale", device)
+    _check(_lib.loom_quantize_rows(_ptr(x), kind, rows, cols, stride, _ptr(q), _ptr(scale), stream), "quantize_rows")
+    return q, scale
+
+
+def i8_matmul(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor | None = None,
+              bias: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """w int32 [rows][k/4], x int32 [tokens][k/4] or [k/4] (packed int8), w_scale f32 [rows], x_scale f32 [tokens],
+    bias f32 [rows] -> out [tokens][rows] of ``dtype`` (or of ``out``, whose rows may be strided)."""
+    device, stream = _target(w, "w")
+    rows, k, tokens, x = _product_operands(w, w_scale, x, x_scale, device)
+    _buffer(bias, torch.float32, rows, "bias", device, optional=True)
+    if out is None:
+        kind = _type(dtype, "dtype")
+        out = torch.empty(tokens, rows, dtype=dtype, device=w.device)
+        stride = rows
+    else:
+        kind = _type(getattr(out, "dtype", None), "out")
+        stride = _rows_of(out, out.dtype, tokens, rows, "out", device)
+    _check(_lib.loom_i8_matmul(_ptr(w), _ptr(w_scale), _ptr(x), _ptr(x_scale), _ptr(bias), rows, k, tokens, _ptr(out),
+                               kind, stride, stream), "i8_matmul")
+    return out
+
+
+def i8_gated_projection(w_gate: torch.Tensor, gate_scale: torch.Tensor, w_up: torch.Tensor, up_scale: torch.Tensor,
+                        x: torch.Tensor, x_scale: torch.Tensor | None = None, act: str = "silu",
+                        dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """act(x w_gate^T) * (x w_up^T) with the scales of i8_matmul -> out [tokens][rows] of ``dtype`` (or of ``out``).
+    act: 'silu', 'gelu', 'gelu_tanh' or 'relu'."""
+    device, stream = _target(w_gate, "w_gate")
+    rows, k, tokens, x = _product_operands(w_gate, gate_scale, x, x_scale, device, "w_gate", "gate_scale")
+    _product_operands(w_up, up_scale, x, x_scale, device, "w_up", "up_scale")
+    _require(w_up.shape == w_gate.shape, "w_up must be shaped as w_gate")
+    code = _act(act)
+    if out is None:
+        kind = _type(dtype, "dtype")
+        out = torch.empty(tokens, rows, dtype=dtype, device=w_gate.device)
+        stride = rows
+    else:
+        kind = _type(getattr(out, "dtype", None), "out")
+        stride = _rows_of(out, out.dtype, tokens, rows, "out", device)
+    _check(_lib.loom_i8_gated_projection(_ptr(w_gate), _ptr(gate_scale), _ptr(w_up), _ptr(up_scale), _ptr(x),
+                                         _ptr(x_scale), rows, k, tokens, code, _ptr(out), kind, stride, stream),
+           "i8_gated_projection")
+    return out
+
+
+def i8_gated_projection_backward_workspace(rows: int, k: int, tokens: int, dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of workspace that i8_gated_projection_backward needs for these sizes and this type of gradient."""
+    n = ctypes.c_int64()
+    _check(_lib.loom_i8_gated_projection_backward_workspace(rows, k, tokens, _type(dtype, "dtype"), ctypes.byref(n)),
+           "i8_gated_projection_backward_workspace")
+    return n.value
+
+
+def i8_gated_projection_backward(w_gate: torch.Tensor, gate_scale: torch.Tensor, w_up: torch.Tensor,
+                                 up_scale: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor | None,
+                                 d_out: torch.Tensor, act: str = "silu", want_d_x: bool = True,
+                                 want_d_scales: bool = True, workspace: torch.Tensor | None = None):
+    """Gradients of i8_gated_projection for d_out [tokens][rows] (f32, f16 or bf16, rows may be strided)
+    -> (d_x [tokens][k] of d_out's type, d_gate_scale f32 [rows], d_up_scale f32 [rows]).
+
+    d_x is the gradient of the dequantised activation x * x_scale.  A gradient that is not wanted is None.
+    workspace: a uint8 buffer of i8_gated_projection_backward_workspace bytes, 16-byte aligned (made here if None)."""
+    device, stream = _target(w_gate, "w_gate")
+    rows, k, tokens, x = _product_operands(w_gate, gate_scale, x, x_scale, device, "w_gate", "gate_scale")
+    _product_operands(w_up, up_scale, x, x_scale, device, "w_up", "up_scale")
+    _require(w_up.shape == w_gate.shape, "w_up must be shaped as w_gate")
+    code = _act(act)
+    kind = _type(getattr(d_out, "dtype", None), "d_out")
+    stride = _rows_of(d_out, d_out.dtype, tokens, rows, "d_out", device)
+    need = i8_gated_projection_backward_workspace(rows, k, tokens, d_out.dtype)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=w_gate.device)
+    _buffer(workspace, torch.uint8, need, "workspace", device)
+    d_x = torch.empty(tokens, k, dtype=d_out.dtype, device=w_gate.device) if want_d_x else None
+    d_gate = torch.empty(rows, dtype=torch.float32, device=w_gate.device) if want_d_scales else None
+    d_up = torch.empty(rows, dtype=torch.float32, device=w_gate.device) if want_d_scales else None
+    _check(_lib.loom_i8_gated_projection_backward(_ptr(w_gate), _ptr(gate_scale), _ptr(w_up), _ptr(up_scale), _ptr(x),
+                                                  _ptr(x_scale), rows, k, tokens, code, _ptr(d_out), kind, stride,
+                                                  _ptr(d_x), _ptr(d_gate), _ptr(d_up), _ptr(workspace),
+                                                  workspace.numel(), stream),
+           "i8_gated_projection_backward")
+    return d_x, d_gate, d_up
 
 
 def pack_int8(t: torch.Tensor) -> torch.Tensor:

@@ -232,3 +232,108 @@ extern "C" int loom_routed_combine(const int32_t *ids, const float *weights, con
                                            out, (hipStream_t)stream);
     });
 }
+
+namespace {
+
+constexpr int64_t element_size(int type) { return type == LOOM_F32 ? 4 : 2; }
+bool known_type(int type) { return type == LOOM_F32 || type == LOOM_F16 || type == LOOM_BF16; }
+bool known_act(int act) { return act >= LOOM_SILU && act <= LOOM_RELU; }
+
+// The size checks shared by the int8 product, the gated projection and its
+// gradients: `stride` is the row stride of the [tokens][rows] matrix.
+int product_sizes(loom::ExportId id, int64_t rows, int64_t k, int64_t tokens, int type, int64_t stride,
+                  loom_launch_config *cfg) {
+    if (k < 0 || k > loom::kMaxK || rows < 0 || rows > kMaxRows || tokens < 0 || tokens > kMaxRows ||
+        !known_type(type))
+        return LOOM_ERR_RANGE;
+    if (k % 4 != 0 || stride < rows) return LOOM_ERR_SHAPE;
+    if (tokens > 0 && stride > (INT64_MAX / 4) / tokens) return LOOM_ERR_RANGE;
+    const int64_t w[3] = {rows, k, tokens};
+    return loom::evaluate_launch(id, w, cfg);
+}
+
+}  // namespace
+
+extern "C" int loom_quantize_rows(const void *x, int type, int64_t rows, int64_t cols, int64_t row_stride, int32_t *q,
+                                  float *scale, void *stream) {
+    if (rows < 0 || rows > kMaxRows || cols < 0 || cols > kMaxRows || !known_type(type)) return LOOM_ERR_RANGE;
+    if (cols % 4 != 0 || row_stride < cols) return LOOM_ERR_SHAPE;
+    if (rows > 0 && row_stride > (INT64_MAX / 4) / rows) return LOOM_ERR_RANGE;
+    loom_launch_config cfg;
+    const int64_t w[2] = {rows, cols};
+    if (int st = loom::evaluate_launch(loom::kQuantizeRows, w, &cfg)) return st;
+    if (rows == 0) return LOOM_OK;
+    if (!scale || (cols > 0 && (!x || !q))) return LOOM_ERR_NULL;
+    if (misaligned(x, element_size(type)) || misaligned(q, 4) || misaligned(scale, 4)) return LOOM_ERR_ALIGN;
+    return launch([&] {
+        return loom::launch_quantize_rows(cfg, x, type, (int)rows, cols, row_stride, q, scale, (hipStream_t)stream);
+    });
+}
+
+extern "C" int loom_i8_matmul(const int32_t *w, const float *w_scale, const int32_t *x, const float *x_scale,
+                              const float *bias, int64_t rows, int64_t k, int64_t tokens, void *out, int type,
+                              int64_t out_stride, void *stream) {
+    loom_launch_config cfg;
+    if (int st = product_sizes(loom::kI8Matmul, rows, k, tokens, type, out_stride, &cfg)) return st;
+    if (rows == 0 || tokens == 0) return LOOM_OK;
+    if (!w_scale || !out || (k > 0 && (!w || !x))) return LOOM_ERR_NULL;
+    if (misaligned(w, 4) || misaligned(x, 4) || misaligned(w_scale, 4) || misaligned(x_scale, 4) ||
+        misaligned(bias, 4) || misaligned(out, element_size(type)))
+        return LOOM_ERR_ALIGN;
+    const loom::I8Product p = {w,         w_scale,     nullptr,        nullptr, x,   x_scale,   bias,
+                               (int)rows, (int)tokens, (int)(k / 4),   0,       out, out_stride};
+    return launch([&] { return loom::launch_i8_matmul(cfg, p, type, (hipStream_t)stream); });
+}
+
+extern "C" int loom_i8_gated_projection(const int32_t *w_gate, const float *gate_scale, const int32_t *w_up,
+                                        const float *up_scale, const int32_t *x, const float *x_scale, int64_t rows,
+                                        int64_t k, int64_t tokens, int act, void *out, int type, int64_t out_stride,
+                                        void *stream) {
+    if (!known_act(act)) return LOOM_ERR_RANGE;
+    loom_launch_config cfg;
+    if (int st = product_sizes(loom::kI8GatedProjection, rows, k, tokens, type, out_stride, &cfg)) return st;
+    if (rows == 0 || tokens == 0) return LOOM_OK;
+    if (!gate_scale || !up_scale || !out || (k > 0 && (!w_gate || !w_up || !x))) return LOOM_ERR_NULL;
+    if (misaligned(w_gate, 4) || misaligned(w_up, 4) || misaligned(x, 4) || misaligned(gate_scale, 4) ||
+        misaligned(up_scale, 4) || misaligned(x_scale, 4) || misaligned(out, element_size(type)))
+        return LOOM_ERR_ALIGN;
+    const loom::I8Product p = {w_gate,    gate_scale,  w_up,         up_scale, x,   x_scale,   nullptr,
+                               (int)rows, (int)tokens, (int)(k / 4), act,      out, out_stride};
+    return launch([&] { return loom::launch_i8_gated_projection(cfg, p, type, (hipStream_t)stream); });
+}
+
+extern "C" int loom_i8_gated_projection_backward_workspace(int64_t rows, int64_t k, int64_t tokens, int type,
+                                                           int64_t *bytes) {
+    if (!bytes) return LOOM_ERR_NULL;
+    loom_launch_config cfg;
+    if (int st = product_sizes(loom::kI8GatedBackward, rows, k, tokens, type, rows, &cfg)) return st;
+    *bytes = loom::gated_backward_workspace_bytes(rows, tokens);
+    return LOOM_OK;
+}
+
+extern "C" int loom_i8_gated_projection_backward(const int32_t *w_gate, const float *gate_scale, const int32_t *w_up,
+                                                 const float *up_scale, const int32_t *x, const float *x_scale,
+                                                 int64_t rows, int64_t k, int64_t tokens, int act, const void *d_out,
+                                                 int type, int64_t d_stride, void *d_x, float *d_gate_scale,
+                                                 float *d_up_scale, void *workspace, int64_t workspace_bytes,
+                                                 void *stream) {
+    if (!known_act(act)) return LOOM_ERR_RANGE;
+    loom_launch_config cfg;
+    if (int st = product_sizes(loom::kI8GatedBackward, rows, k, tokens, type, d_stride, &cfg)) return st;
+    if (workspace_bytes < loom::gated_backward_workspace_bytes(rows, tokens)) return LOOM_ERR_RANGE;
+    if ((!d_x || tokens == 0 || k == 0) && ((!d_gate_scale && !d_up_scale) || rows == 0)) return LOOM_OK;
+    if (rows > 0 && tokens > 0 &&
+        (!gate_scale || !up_scale || !d_out || !workspace || (k > 0 && (!w_gate || !w_up || !x))))
+        return LOOM_ERR_NULL;
+    if (misaligned(w_gate, 4) || misaligned(w_up, 4) || misaligned(x, 4) || misaligned(gate_scale, 4) ||
+        misaligned(up_scale, 4) || misaligned(x_scale, 4) || misaligned(d_out, element_size(type)) ||
+        misaligned(d_x, element_size(type)) || misaligned(d_gate_scale, 4) || misaligned(d_up_scale, 4) ||
+        misaligned(workspace, 16))
+        return LOOM_ERR_ALIGN;
+    const loom::I8Product p = {w_gate,    gate_scale,  w_up,         up_scale, x,       x_scale, nullptr,
+                               (int)rows, (int)tokens, (int)(k / 4), act,      nullptr, 0};
+    return launch([&] {
+        return loom::launch_i8_gated_projection_backward(cfg, p, d_out, type, d_stride, d_x, d_gate_scale, d_up_scale,
+                                                         workspace, (hipStream_t)stream);
+    });
+}

@@ -1,0 +1,70 @@
+// ffn_common.hpp -- element types and activations shared by the int8
+// feed-forward kernels (row quantiser, product, gated projection, gradients).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.hpp"
+#include "internal.hpp"
+
+namespace loom {
+
+template <int TYPE> struct ElementOf;
+template <> struct ElementOf<LOOM_F32> { typedef float type; };
+template <> struct ElementOf<LOOM_F16> { typedef _Float16 type; };
+template <> struct ElementOf<LOOM_BF16> { typedef __bf16 type; };
+
+// Phi(g), the normal distribution's integral: erfc keeps the lower tail's
+// relative accuracy, which 1 + erf loses.
+__device__ __forceinline__ float normal_cdf(float g) { return 0.5f * erfcf(g * -0.70710678118654752f); }
+
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+// The tanh form's factor 0.5 (1 + tanh z), z = sqrt(2/pi) (g + 0.044715 g^3),
+// is sigmoid(2 z).  It is 0 or 1 to f32 well inside |g| = 16, where g is held
+// so that its powers stay finite; a NaN passes.
+__device__ __forceinline__ float tanh_form_gate(float g) { return g > 16.0f ? 16.0f : g < -16.0f ? -16.0f : g; }
+__device__ __forceinline__ float tanh_form_cdf(float c) {
+    return sigmoid(1.5957691216057308f * (c + 0.044715f * c * c * c));
+}
+
+// act(g) of a gated unit.  A NaN stays a NaN in each of them; 1 + exp(-g)
+// overflows to infinity for g < -88, where the rounded value is 0.
+__device__ __forceinline__ float act_value(int act, float g) {
+    switch (act) {
+        case LOOM_SILU: return g / (1.0f + expf(-g));
+        case LOOM_GELU: return g * normal_cdf(g);
+        case LOOM_GELU_TANH: return g * tanh_form_cdf(tanh_form_gate(g));
+        default: return g < 0.0f ? 0.0f : g;
+    }
+}
+
+// act(g) and its derivative.  ReLU's derivative at 0 is 0.
+__device__ __forceinline__ void act_value_slope(int act, float g, float &value, float &slope) {
+    switch (act) {
+        case LOOM_SILU: {
+            const float p = sigmoid(g);
+            value = g * p;
+            slope = p * (1.0f + g * (1.0f - p));
+            return;
+        }
+        case LOOM_GELU: {
+            const float p = normal_cdf(g);
+            value = g * p;
+            slope = p + g * expf(-0.5f * g * g) * 0.39894228040143268f;
+            return;
+        }
+        case LOOM_GELU_TANH: {
+            const float c = tanh_form_gate(g), p = tanh_form_cdf(c);
+            value = g * p;
+            slope = p + c * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * c * c);
+            return;
+        }
+        default:
+            value = g < 0.0f ? 0.0f : g;
+            slope = g > 0.0f ? 1.0f : g != g ? g : 0.0f;
+    }
+}
+
+}  // namespace loom

@@ -18,6 +18,10 @@ enum ExportId : uint32_t {
     kPackedDot,
     kSumGuardedRows,
     kRoutedCombine,
+    kQuantizeRows,
+    kI8Matmul,
+    kI8GatedProjection,
+    kI8GatedBackward,
     kExportCount
 };
 
@@ -402,6 +406,33 @@ constexpr uint32_t i8_rows_lds_bytes(int chunks) {
 constexpr int kMaxBatch = 64;
 constexpr int64_t kMaxK = 131068;
 
+// A row whose largest magnitude is below 2^-119 quantises to zeros: 127 times
+// its reciprocal could leave the f32 range, and its scale would be subnormal.
+constexpr float kQuantizeTiny = 0x1p-119f;
+
+// The operands of the int8 product and of the gated projection (w, w_scale
+// are then the gate's, w_up, up_scale the other projection's).
+struct I8Product {
+    const int32_t *w;       // [rows][kw]
+    const float *w_scale;   // [rows]
+    const int32_t *w_up;    // [rows][kw], gated only
+    const float *up_scale;  // [rows], gated only
+    const int32_t *x;       // [tokens][kw]
+    const float *x_scale;   // [tokens] or NULL (= 1)
+    const float *bias;      // [rows] or NULL, product only
+    int rows, tokens, kw;   // kw: words of a row
+    int act;                // loom_activation, gated only
+    void *out;              // [tokens][out_stride]
+    int64_t out_stride;
+};
+
+// Device memory of the gated projection's gradients: the coefficients of d_x
+// (two a token and channel) and the scale gradients' partial sums (two a
+// token tile and channel).
+constexpr int64_t gated_backward_workspace_bytes(int64_t rows, int64_t tokens) {
+    return 8 * rows * (tokens + (tokens + 15) / 16);
+}
+
 // Kernel launchers.  Arguments are already validated; geometry comes from
 // evaluate_launch.  Each returns the HIP launch status.
 hipError_t launch_copy_f32(const loom_launch_config &cfg, const float *in, float *out, int64_t n,
@@ -433,5 +464,19 @@ hipError_t launch_sum_guarded_rows(const loom_launch_config &cfg, const float *v
 hipError_t launch_routed_combine(const loom_launch_config &cfg, const int32_t *ids, const float *weights,
                                  const float *payload, int64_t num_rows, int64_t tokens, int routes, int hidden,
                                  float *out, hipStream_t stream);
+
+hipError_t launch_quantize_rows(const loom_launch_config &cfg, const void *x, int type, int rows, int64_t cols,
+                                int64_t row_stride, int32_t *q, float *scale, hipStream_t stream);
+
+hipError_t launch_i8_matmul(const loom_launch_config &cfg, const I8Product &p, int type, hipStream_t stream);
+
+hipError_t launch_i8_gated_projection(const loom_launch_config &cfg, const I8Product &p, int type,
+                                      hipStream_t stream);
+
+// type, d_stride: of d_out; d_x (same type), d_gate and d_up may each be NULL
+// (not wanted).
+hipError_t launch_i8_gated_projection_backward(const loom_launch_config &cfg, const I8Product &p, const void *d_out,
+                                               int type, int64_t d_stride, void *d_x, float *d_gate, float *d_up,
+                                               void *workspace, hipStream_t stream);
 
 }  // namespace loom

@@ -150,6 +150,21 @@ int geo_routed_combine(const int64_t *w, loom_launch_config *c) {
                 0);
 }
 
+// quantize_rows(rows, cols): one workgroup per row, each taking every
+// grid.x-th row once the grid reaches the work-item limit.
+int geo_quantize_rows(const int64_t *w, loom_launch_config *c) {
+    if (w[0] < 0 || w[1] < 0) return LOOM_ERR_RANGE;
+    return set(c, grid_stride_groups(w[0], 256), 256, 256 * 4);
+}
+
+// i8_matmul, i8_gated_projection and its gradients (rows, k, tokens): one
+// workgroup per 16 channels x 16 tokens.
+int geo_i8_product(const int64_t *w, loom_launch_config *c) {
+    if (w[0] < 0 || w[1] < 0 || w[2] < 0) return LOOM_ERR_RANGE;
+    if (w[0] > 0 && ceil_div(w[2], 16) > kMaxGridWorkItems / ceil_div(w[0], 16)) return LOOM_ERR_RANGE;
+    return set(c, ceil_div(w[0], 16) * ceil_div(w[2], 16), 256, 0);
+}
+
 struct Export {
     const char *name;
     size_t arity;
@@ -165,6 +180,10 @@ const Export kExports[kExportCount] = {
     {"packed_dot", 3, geo_packed_dot},
     {"sum_guarded_rows", 1, geo_sum_guarded_rows},
     {"routed_combine", 3, geo_routed_combine},
+    {"quantize_rows", 2, geo_quantize_rows},
+    {"i8_matmul", 3, geo_i8_product},
+    {"i8_gated_projection", 3, geo_i8_product},
+    {"i8_gated_projection_backward", 3, geo_i8_product},
 };
 
 }  // namespace
