@@ -382,7 +382,7 @@ int loom_i8_matmul(const int32_t *w, const float *w_scale, const int32_t *x, con
  * (no bias) for the two weights,                                            *
  *     out[t][n] = act(g[t][n]) * u[t][n]                                    *
  * in f32, rounded once to the output type.  Arguments as there, each for    *
- * both weights; act is a loom_activation (LOOM_ERR_RANGE otherwise).        *
+ * both weights; act is a loom_activation, anything else LOOM_ERR_RANGE.      *
  * ------------------------------------------------------------------------ */
 int loom_i8_gated_projection(const int32_t *w_gate, const float *gate_scale, const int32_t *w_up,
                              const float *up_scale, const int32_t *x, const float *x_scale, int64_t rows, int64_t k,

@@ -6,39 +6,188 @@
 //     y[t][n]   = (f32(acc[t][n]) * w_scale[n]) * x_scale[t]    (two f32 roundings)
 //     product:  out[t][n] = y[t][n] + bias[n]
 //     gated:    out[t][n] = act(y_gate[t][n]) * y_up[t][n]
-#include "ffn_common.hpp"
+#include "i8_tiles.hpp"
 
 namespace loom {
 
 namespace {
 
-// One output per thread, 16 tokens x 16 channels per workgroup.
-template <bool GATED, int TYPE>
-__global__ __launch_bounds__(256) void i8_product_kernel(I8Product p) {
-    typedef typename ElementOf<TYPE>::type T;
-    const int64_t tiles = (p.rows + 15) / 16;
-    const int64_t n = (int64_t)(blockIdx.x % tiles) * 16 + (threadIdx.x & 15);
-    const int64_t t = (int64_t)(blockIdx.x / tiles) * 16 + (threadIdx.x >> 4);
-    if (n >= p.rows || t >= p.tokens) return;
-    const int32_t *xr = p.x + t * p.kw, *wr = p.w + n * p.kw, *ur = GATED ? p.w_up + n * p.kw : nullptr;
-    int acc = 0, up = 0;
-    for (int j = 0; j < p.kw; ++j) {
-        acc = __builtin_amdgcn_sdot4(wr[j], xr[j], acc, false);
-        if (GATED) up = __builtin_amdgcn_sdot4(ur[j], xr[j], up, false);
+// Up to 16 tokens: the weights stream once from memory, straight into the matrix
+// cores' operand registers.  A workgroup owns 16 weight rows (gated: 8 gate rows
+// and the same 8 up rows); its KS waves each take a contiguous share of k in
+// records of 16 rows x 256 bytes, and their int32 partial sums are added in wave
+// order.  One load instruction reads 4 rows x 256 contiguous bytes: lane l holds
+// bytes 64 (l & 3) + 16 (l >> 4) .. + 15 of row 4 i + (l >> 2 & 3), so the
+// product's 16 rows are 4 weight rows x 4 segments of 64 bytes, and the 16 columns
+// of B are 4 tokens x the same 4 segments.  Of the sums only those of equal
+// segments are wanted: element e = l & 3 of lane l, row 4 i + (l >> 4), token
+// 4 v + (l >> 2 & 3); a quad's four lanes hold the four segments of one output.
+// The matrix cores do 4 times the useful products, a tenth of their time here;
+// in exchange the stream needs no LDS and every load reads whole lines.
+template <int VG>
+struct StreamRecord {
+    int4v a[4], b[VG];
+};
+
+typedef int int4u __attribute__((ext_vector_type(4), aligned(4)));
+
+template <bool GATED, int VG>
+__global__ __launch_bounds__(kWave * kI8StreamWaves) void i8_stream_kernel(I8Product p, int type) {
+    constexpr int KS = kI8StreamWaves;
+    constexpr int kRecordWords = 64;
+    constexpr int kOuts = 16 * 4 * VG, OC = GATED ? 8 : 16;
+    __shared__ int part[KS][kOuts];
+    const int lane = lane_id(), m = lane & 15, g = lane >> 4;
+    // the same in every lane: keeps the wave's share of k and its loop scalar
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    const int64_t n0 = (int64_t)blockIdx.x * OC;
+    const int left = (int)min((int64_t)OC, p.rows - n0);
+    const int at = (m & 3) * 16 + g * 4;
+    const int32_t *wrow[4], *xrow[VG];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int slot = 4 * i + (m >> 2);
+        wrow[i] = (GATED && slot >= 8 ? p.w_up : p.w) + (n0 + min(slot % OC, left - 1)) * p.kw;
     }
-    const float xs = p.x_scale ? p.x_scale[t] : 1.0f;
-    float y = (float)acc * p.w_scale[n] * xs;
-    if (GATED) y = act_value(p.act, y) * ((float)up * p.up_scale[n] * xs);
-    else if (p.bias) y = y + p.bias[n];
-    ((T *)p.out)[t * p.out_stride + n] = (T)y;
+    bool live[VG];
+#pragma unroll
+    for (int v = 0; v < VG; ++v) {
+        live[v] = 4 * v + (m >> 2) < p.tokens;
+        xrow[v] = p.x + (int64_t)min(4 * v + (m >> 2), p.tokens - 1) * p.kw;
+    }
+    const int all = p.kw / kRecordWords, per_wave = (all + KS - 1) / KS;
+    const int first = min(all, wave * per_wave), records = min(all, first + per_wave) - first;
+    int4v acc[4][VG];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int v = 0; v < VG; ++v) acc[i][v] = int4v{0, 0, 0, 0};
+    auto consume = [&](const StreamRecord<VG> &q) {
+#pragma unroll
+        for (int v = 0; v < VG; ++v) {
+            const int4v b = live[v] ? q.b[v] : int4v{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i][v] = __builtin_amdgcn_mfma_i32_16x16x64_i8(q.a[i], b, acc[i][v], 0, 0, 0);
+        }
+    };
+    int c = first * kRecordWords + at;
+    pipelined<2, StreamRecord<VG>>(
+        records,
+        [&]() {
+            StreamRecord<VG> q;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q.a[i] = __builtin_nontemporal_load((const int4u *)(wrow[i] + c));
+#pragma unroll
+            for (int v = 0; v < VG; ++v) q.b[v] = *(const int4u *)(xrow[v] + c);
+            c += kRecordWords;
+            return q;
+        },
+        consume);
+    if (p.kw % kRecordWords && wave == KS - 1) {  // the rest of the row: words past it are zero
+        StreamRecord<VG> q;
+        auto guarded = [&](const int32_t *row) {
+            int4v v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = all * kRecordWords + at + e;
+                v[e] = j < p.kw ? row[j < p.kw ? j : 0] : 0;
+            }
+            return v;
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q.a[i] = guarded(wrow[i]);
+#pragma unroll
+        for (int v = 0; v < VG; ++v) q.b[v] = guarded(xrow[v]);
+        consume(q);
+    }
+    // each quad adds its output's 4 segments; its first lane publishes the sum
+    const int e = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int v = 0; v < VG; ++v) {
+            const int4v d = acc[i][v];
+            int t = e == 0 ? d[0] : e == 1 ? d[1] : e == 2 ? d[2] : d[3];
+            t = t + dpp<kDppQuadSwap1>(t);
+            t = t + dpp<kDppQuadSwap2>(t);
+            if (e == 0) part[wave][(4 * v + (m >> 2)) * 16 + 4 * i + g] = t;
+        }
+    __syncthreads();
+    for (int o = threadIdx.x; o < OC * 4 * VG; o += kWave * KS) {
+        const int t = o / OC, r = o % OC;
+        if (t >= p.tokens || r >= left) continue;
+        int sum = 0, up = 0;
+#pragma unroll
+        for (int q = 0; q < KS; ++q) {
+            sum += part[q][t * 16 + r];
+            if (GATED) up += part[q][t * 16 + 8 + r];
+        }
+        const int64_t n = n0 + r;
+        const float xs = p.x_scale ? p.x_scale[t] : 1.0f;
+        float y = (float)sum * p.w_scale[n] * xs;
+        if (GATED) y = act_value(p.act, y) * ((float)up * p.up_scale[n] * xs);
+        else if (p.bias) y = y + p.bias[n];
+        store1(p.out, type, t * p.out_stride + n, y);
+    }
+}
+
+template <typename C>
+__global__ __launch_bounds__(C::NW * kWave, 1) void i8_tile_kernel(I8Product p, int type) {
+    __shared__ __align__(1024) char lds[C::kLds];
+    uint32_t ch, tok;
+    tile_of(blockIdx.x, (p.rows + C::OUT_CH - 1) / C::OUT_CH, (p.tokens + C::TK - 1) / C::TK, 8, ch, tok);
+    TileLoop<C> loop(p, lds, (int64_t)ch * C::OUT_CH, (int64_t)tok * C::TK);
+    int4v acc[C::WT][C::XT];
+#pragma unroll
+    for (int i = 0; i < C::WT; ++i)
+#pragma unroll
+        for (int x = 0; x < C::XT; ++x) acc[i][x] = int4v{};
+    const int steps = p.kw / 32;
+    loop.run(acc, p.tokens <= C::TK && steps > 0 ? (int)(ch * 5 % steps) : 0);
+    const bool whole = p.out_stride % 4 == 0 && (uintptr_t)p.out % (4 * element_bytes(type)) == 0;
+    const int64_t n = TileOut<C>::out_channel(loop), left = p.rows - n;
+    float ws[4], us[4], bias[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int64_t m = min(n + e, (int64_t)p.rows - 1);
+        ws[e] = p.w_scale[m];
+        us[e] = C::GATED ? p.up_scale[m] : 1.0f;
+        bias[e] = !C::GATED && p.bias ? p.bias[m] : 0.0f;
+    }
+    TileOut<C>::each(loop, acc, [&](int64_t t, float xs, int4v a, int4v u) {
+        if (left <= 0) return;
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            y[e] = (float)a[e] * ws[e] * xs;
+            if constexpr (C::GATED) y[e] = act_value(p.act, y[e]) * ((float)u[e] * us[e] * xs);
+            else if (p.bias) y[e] = y[e] + bias[e];
+        }
+        store4(p.out, type, t * p.out_stride + n, left, whole, y);
+    });
+}
+
+template <bool GATED, int SHAPE = 0>
+void launch_tile(int shape, dim3 grid, dim3 block, const I8Product &p, int type, hipStream_t stream) {
+    if constexpr (SHAPE < kI8TileCount) {
+        if (shape != SHAPE) return launch_tile<GATED, SHAPE + 1>(shape, grid, block, p, type, stream);
+        hipLaunchKernelGGL((i8_tile_kernel<TileConfig<GATED, SHAPE>>), grid, block, 0, stream, p, type);
+    }
 }
 
 template <bool GATED>
 hipError_t run(const loom_launch_config &cfg, const I8Product &p, int type, hipStream_t stream) {
     const dim3 grid(cfg.workgroups[0]), block(cfg.workgroup_size[0]);
-    if (type == LOOM_F32) hipLaunchKernelGGL((i8_product_kernel<GATED, LOOM_F32>), grid, block, 0, stream, p);
-    else if (type == LOOM_F16) hipLaunchKernelGGL((i8_product_kernel<GATED, LOOM_F16>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((i8_product_kernel<GATED, LOOM_BF16>), grid, block, 0, stream, p);
+    if (p.tokens > i8_stream_max_tokens(GATED)) {
+        launch_tile<GATED>(i8_tile_choice(p.rows, 4 * (int64_t)p.kw, p.tokens, GATED), grid, block, p, type, stream);
+        return hipGetLastError();
+    }
+    switch (i8_stream_groups(p.tokens)) {
+        case 1: hipLaunchKernelGGL((i8_stream_kernel<GATED, 1>), grid, block, 0, stream, p, type); break;
+        case 2: hipLaunchKernelGGL((i8_stream_kernel<GATED, 2>), grid, block, 0, stream, p, type); break;
+        default:
+            if constexpr (!GATED) hipLaunchKernelGGL((i8_stream_kernel<false, 4>), grid, block, 0, stream, p, type);
+    }
     return hipGetLastError();
 }
 

@@ -410,6 +410,69 @@ constexpr int64_t kMaxK = 131068;
 // its reciprocal could leave the f32 range, and its scale would be subnormal.
 constexpr float kQuantizeTiny = 0x1p-119f;
 
+// The kernels of the int8 product and the gated projection.  Up to 8 tokens (16
+// for the product) stream the weights through registers (i8_stream_kernel: 16
+// weight rows a workgroup, 4 waves that split k); more go through LDS tiles of
+// one of these shapes.
+struct I8TileShape {
+    int wm, wn, wt, xt;          // waves over channels and tokens, 16 x 16 blocks of a wave
+    int ring_w, ring_x;          // steps of 128 bytes of k in LDS
+    int resident;                // workgroups of a CU
+    double step_us;              // one step of a workgroup that has its CU to itself
+    constexpr int channels() const { return wm * wt * 16; }
+    constexpr int tokens() const { return wn * xt * 16; }
+    constexpr int waves() const { return wm * wn; }
+    constexpr int lds() const { return (ring_w * channels() + ring_x * tokens()) * 128; }
+};
+constexpr I8TileShape kI8Tiles[] = {
+    {1, 2, 2, 1, 5, 5, 4, 0.21}, {2, 2, 2, 1, 6, 6, 2, 0.27}, {2, 2, 2, 2, 5, 5, 2, 0.29}, {2, 2, 4, 2, 3, 3, 2, 0.40},
+    {2, 2, 2, 4, 3, 3, 2, 0.36}, {2, 2, 4, 4, 5, 5, 1, 0.54}, {2, 2, 4, 8, 4, 3, 1, 0.85}, {2, 2, 8, 8, 2, 2, 1, 1.27}};
+constexpr int kI8TileCount = 8;
+constexpr int kI8StreamWaves = 4;  // 1, 2 and 8 waves were up to 30, 8 and 20 % slower, rarely faster
+constexpr int kI8StreamRows = 16;
+constexpr int i8_stream_max_tokens(bool gated) { return gated ? 8 : 16; }
+constexpr int i8_stream_groups(int64_t tokens) { return tokens <= 4 ? 1 : tokens <= 8 ? 2 : 4; }
+
+constexpr int64_t ceil_of(int64_t a, int64_t b) { return a / b + (a % b != 0); }
+constexpr int64_t i8_tile_count(const I8TileShape &t, int64_t rows, int64_t tokens, bool gated) {
+    return ceil_of(rows, t.channels() / (gated ? 2 : 1)) * ceil_of(tokens, t.tokens());
+}
+
+// The tile shape (an index of kI8Tiles) with the least estimated time.  A round
+// of r workgroups a CU takes, for each step, the longest of its own latency
+// (step_us, measured), the bytes of r steps at 58 KB/us (what a CU's direct loads
+// reach from its L2) and their products at 16.4 M operations/us; the launch takes
+// its rounds, or the memory's time for the weights at 6 TB/s if that is longer.
+// Over 156 sizes (500 to 28672 channels, 17 to 2048 tokens, k 1024 to 28672) the
+// shape so chosen took 1 % longer on average than the fastest of the eight, at
+// worst 14 %; the 256 x 256 shape alone took 3 times as long on average.
+constexpr int i8_tile_choice(int64_t rows, int64_t k, int64_t tokens, bool gated) {
+    int best = 0;
+    double best_us = 0;
+    for (int i = 0; i < kI8TileCount; ++i) {
+        const I8TileShape &t = kI8Tiles[i];
+        const int64_t tiles = i8_tile_count(t, rows, tokens, gated), round = 256 * t.resident;
+        const int64_t full = tiles / round, rest = ceil_of(tiles % round, 256);
+        double us = 0;
+        for (int last = 0; last < 2; ++last) {
+            const double r = last ? (double)rest : (double)t.resident, times = last ? (rest > 0) : (double)full;
+            double step = t.step_us;
+            const double load = r * (t.channels() + t.tokens()) * 128 / 58e3;
+            const double math = r * t.channels() * t.tokens() * 256.0 / 16.4e6;
+            if (load > step) step = load;
+            if (math > step) step = math;
+            us += times * (step * (double)k / 128 + 1);
+        }
+        const double memory = ((double)rows * (gated ? 2 : 1) + (double)tokens) * (double)k / 6e6;
+        if (memory > us) us = memory;
+        if (i == 0 || us < best_us) {
+            best = i;
+            best_us = us;
+        }
+    }
+    return best;
+}
+
 // The operands of the int8 product and of the gated projection (w, w_scale
 // are then the gate's, w_up, up_scale the other projection's).
 struct I8Product {

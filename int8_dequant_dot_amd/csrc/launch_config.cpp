@@ -157,9 +157,25 @@ int geo_quantize_rows(const int64_t *w, loom_launch_config *c) {
     return set(c, grid_stride_groups(w[0], 256), 256, 256 * 4);
 }
 
-// i8_matmul, i8_gated_projection and its gradients (rows, k, tokens): one
-// workgroup per 16 channels x 16 tokens.
+// i8_matmul, i8_gated_projection (rows, k, tokens): few tokens take one
+// workgroup per kI8StreamRows weight rows (LDS: its waves' partial sums); more
+// take one per tile of i8_tile_choice.
+int geo_i8_tiles(const int64_t *w, bool gated, loom_launch_config *c) {
+    const I8TileShape &t = kI8Tiles[i8_tile_choice(w[0], w[1], w[2], gated)];
+    return set(c, i8_tile_count(t, w[0], w[2], gated), (uint32_t)(t.waves() * kSubgroupSize), (uint32_t)t.lds());
+}
+template <bool GATED>
 int geo_i8_product(const int64_t *w, loom_launch_config *c) {
+    if (w[0] < 0 || w[1] < 0 || w[2] < 0) return LOOM_ERR_RANGE;
+    if (w[2] > i8_stream_max_tokens(GATED)) return geo_i8_tiles(w, GATED, c);
+    const int64_t groups = w[2] > 0 ? ceil_div(w[0], kI8StreamRows / (GATED ? 2 : 1)) : 0;
+    return set(c, groups, kI8StreamWaves * kSubgroupSize,
+               (uint32_t)(kI8StreamWaves * kI8StreamRows * 16 * i8_stream_groups(w[2])));
+}
+
+// i8_gated_projection_backward(rows, k, tokens): its first kernel, one
+// workgroup per 16 channels x 16 tokens.
+int geo_i8_backward(const int64_t *w, loom_launch_config *c) {
     if (w[0] < 0 || w[1] < 0 || w[2] < 0) return LOOM_ERR_RANGE;
     if (w[0] > 0 && ceil_div(w[2], 16) > kMaxGridWorkItems / ceil_div(w[0], 16)) return LOOM_ERR_RANGE;
     return set(c, ceil_div(w[0], 16) * ceil_div(w[2], 16), 256, 0);
@@ -181,9 +197,9 @@ const Export kExports[kExportCount] = {
     {"sum_guarded_rows", 1, geo_sum_guarded_rows},
     {"routed_combine", 3, geo_routed_combine},
     {"quantize_rows", 2, geo_quantize_rows},
-    {"i8_matmul", 3, geo_i8_product},
-    {"i8_gated_projection", 3, geo_i8_product},
-    {"i8_gated_projection_backward", 3, geo_i8_product},
+    {"i8_matmul", 3, geo_i8_product<false>},
+    {"i8_gated_projection", 3, geo_i8_product<true>},
+    {"i8_gated_projection_backward", 3, geo_i8_backward},
 };
 
 }  // namespace
