@@ -406,6 +406,7 @@ int loom_i8_gated_projection(const int32_t *w_gate, const float *gate_scale, con
  *                  that loom_i8_gated_projection_backward_workspace gives   *
  *                  for the same sizes (LOOM_ERR_RANGE); its contents after  *
  *                  the call mean nothing                                    *
+ *   rows         : 0 <= rows <= 2^21 (LOOM_ERR_RANGE)                     *
  * With no tokens the scale gradients are 0, with no channels d_x is.        *
  * ------------------------------------------------------------------------ */
 int loom_i8_gated_projection_backward_workspace(int64_t rows, int64_t k, int64_t tokens, int type, int64_t *bytes);

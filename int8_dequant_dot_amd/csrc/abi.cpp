@@ -307,7 +307,7 @@ extern "C" int loom_i8_gated_projection_backward_workspace(int64_t rows, int64_t
     if (!bytes) return LOOM_ERR_NULL;
     loom_launch_config cfg;
     if (int st = product_sizes(loom::kI8GatedBackward, rows, k, tokens, type, rows, &cfg)) return st;
-    *bytes = loom::gated_backward_workspace_bytes(rows, tokens);
+    *bytes = loom::gated_backward_workspace_bytes(rows, k, tokens, type);
     return LOOM_OK;
 }
 
@@ -320,7 +320,7 @@ extern "C" int loom_i8_gated_projection_backward(const int32_t *w_gate, const fl
     if (!known_act(act)) return LOOM_ERR_RANGE;
     loom_launch_config cfg;
     if (int st = product_sizes(loom::kI8GatedBackward, rows, k, tokens, type, d_stride, &cfg)) return st;
-    if (workspace_bytes < loom::gated_backward_workspace_bytes(rows, tokens)) return LOOM_ERR_RANGE;
+    if (workspace_bytes < loom::gated_backward_workspace_bytes(rows, k, tokens, type)) return LOOM_ERR_RANGE;
     if ((!d_x || tokens == 0 || k == 0) && ((!d_gate_scale && !d_up_scale) || rows == 0)) return LOOM_OK;
     if (rows > 0 && tokens > 0 &&
         (!gate_scale || !up_scale || !d_out || !workspace || (k > 0 && (!w_gate || !w_up || !x))))

@@ -15,7 +15,7 @@ template <> struct ElementOf<LOOM_F32> { typedef float type; };
 template <> struct ElementOf<LOOM_F16> { typedef _Float16 type; };
 template <> struct ElementOf<LOOM_BF16> { typedef __bf16 type; };
 
-__device__ __forceinline__ constexpr int element_bytes(int type) { return type == LOOM_F32 ? 4 : 2; }
+__host__ __device__ __forceinline__ constexpr int element_bytes(int type) { return type == LOOM_F32 ? 4 : 2; }
 
 // One value, or four neighbours (one store where `whole` says the row allows
 // it, or the first `left`), rounded once to the output type; the branch on the
@@ -36,6 +36,30 @@ __device__ __forceinline__ void store4(void *out, int type, int64_t at, int64_t 
     if (type == LOOM_F32) store4_as((float *)out + at, left, whole, y);
     else if (type == LOOM_F16) store4_as((_Float16 *)out + at, left, whole, y);
     else store4_as((__bf16 *)out + at, left, whole, y);
+}
+__device__ __forceinline__ float load1(const void *in, int type, int64_t at) {
+    if (type == LOOM_F32) return ((const float *)in)[at];
+    if (type == LOOM_F16) return (float)((const _Float16 *)in)[at];
+    return (float)((const __bf16 *)in)[at];
+}
+template <typename T>
+__device__ __forceinline__ void load4_as(const T *from, int64_t left, bool whole, float (&y)[4]) {
+    typedef T V __attribute__((ext_vector_type(4)));
+    if (whole && left >= 4) {
+        const V v = *(const V *)from;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = (float)v[e];
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = e < left ? (float)from[e] : 0.0f;
+}
+// Four neighbours, 0 past the first `left`.
+__device__ __forceinline__ void load4(const void *in, int type, int64_t at, int64_t left, bool whole,
+                                      float (&y)[4]) {
+    if (type == LOOM_F32) load4_as((const float *)in + at, left, whole, y);
+    else if (type == LOOM_F16) load4_as((const _Float16 *)in + at, left, whole, y);
+    else load4_as((const __bf16 *)in + at, left, whole, y);
 }
 __device__ __forceinline__ void store1(void *out, int type, int64_t at, float y) {
     if (type == LOOM_F32) ((float *)out)[at] = y;
@@ -86,7 +110,7 @@ __device__ __forceinline__ void act_value_slope(int act, float g, float &value, 
         case LOOM_GELU: {
             const float p = normal_cdf(g);
             value = g * p;
-            slope = p + g * expf(-0.5f * g * g) * 0.39894228040143268f;
+            slope = p + g * __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f) * 0.39894228040143268f;
             return;
         }
         case LOOM_GELU_TANH: {

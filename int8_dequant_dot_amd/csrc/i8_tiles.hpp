@@ -336,12 +336,13 @@ struct TileOut {
     static constexpr int BLOCKS = FIT >= C::XT ? C::XT : FIT >= 4 && C::XT % 4 == 0 ? 4 : FIT >= 2 && C::XT % 2 == 0 ? 2 : 1;  // token blocks at a time
     static_assert(C::XT % BLOCKS == 0 && LANES <= kWave && kWave % LANES == 0 && FIT > 0, "whole passes");
 
-    static __device__ int64_t out_channel(const TileLoop<C> &l) {
+    template <typename Loop>
+    static __device__ int64_t out_channel(const Loop &l) {
         return l.n0 + l.wm * OC + 4 * (l.lane % LANES);
     }
 
-    template <typename Use>
-    static __device__ __forceinline__ void each(const TileLoop<C> &l, int4v (&acc)[C::WT][C::XT], Use &&use) {
+    template <typename Loop, typename Use>
+    static __device__ __forceinline__ void each(const Loop &l, int4v (&acc)[C::WT][C::XT], Use &&use) {
         char *mine = l.lds + l.wave * ROOM;
         float *scales = (float *)(mine + ROOM - 64 * C::XT);
         const int m = l.lane & 15, g = l.lane >> 4, c = l.lane % LANES;

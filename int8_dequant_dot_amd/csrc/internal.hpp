@@ -489,11 +489,66 @@ struct I8Product {
     int64_t out_stride;
 };
 
-// Device memory of the gated projection's gradients: the coefficients of d_x
-// (two a token and channel) and the scale gradients' partial sums (two a
-// token tile and channel).
-constexpr int64_t gated_backward_workspace_bytes(int64_t rows, int64_t tokens) {
-    return 8 * rows * (tokens + (tokens + 15) / 16);
+// The gradients of the gated projection.  The first kernel computes both
+// products again in tiles of i8_tile_choice and leaves the coefficients of d_x,
+// bfloat16 [limbs][tokens][2][channels, padded with zeros to 64] (a coefficient
+// is the sum of its limbs: 8 bits each, one for bfloat16 gradients, 2 for float16,
+// 3 for float32), and each token tile's terms of the scale gradients.  The second
+// multiplies the coefficients by the weights, in tiles of one of these shapes
+// (columns of d_x x tokens), its steps split over workgroups where the tiles are
+// few; a third adds the parts.
+constexpr int kI8ChannelPad = 64;
+constexpr int64_t kI8BackwardMaxRows = (int64_t)1 << 21;  // 32-bit offsets within a token tile's coefficients
+constexpr int i8_limbs(int type) { return type == LOOM_BF16 ? 1 : type == LOOM_F16 ? 2 : 3; }
+struct I8DxShape {
+    int wm, wn, it, xt;          // waves over columns and tokens, 16 x 16 blocks of a wave
+    constexpr int columns() const { return wm * it * 16; }
+    constexpr int tokens() const { return wn * xt * 16; }
+    constexpr int step_bytes(int limbs) const { return 64 * columns() + limbs * tokens() * 128; }
+    constexpr int waves() const { return wm * wn; }
+    // steps of 64 channels in LDS
+    constexpr int ring(int limbs) const {
+        const int wide = columns() > 128;
+        const int fit = (wide ? 160 : 80) * 1024 / step_bytes(limbs);
+        return fit > 5 ? 5 : fit >= 2 ? fit : 2;
+    }
+    constexpr int resident(int limbs) const { return 160 * 1024 / (ring(limbs) * step_bytes(limbs)); }
+};
+constexpr I8DxShape kI8Dx[] = {{2, 2, 8, 8}, {2, 2, 4, 4}, {4, 1, 2, 2}};
+struct I8DxPlan {
+    int shape, splits;
+    int64_t tiles;
+};
+constexpr int64_t i8_dx_steps(int64_t rows) { return 2 * ceil_of(rows, kI8ChannelPad); }
+constexpr I8DxPlan i8_dx_plan(int64_t rows, int64_t k, int64_t tokens, int type) {
+    const int limbs = i8_limbs(type);
+    int shape = tokens <= 32 ? 2 : 1;
+    if (limbs == 1 && ceil_of(k, 256) * ceil_of(tokens, 256) >= 160) shape = 0;
+    const I8DxShape &s = kI8Dx[shape];
+    const int64_t tiles = ceil_of(k, s.columns()) * ceil_of(tokens, s.tokens());
+    const int64_t slots = 256 * s.resident(limbs);
+    int64_t splits = tiles > 0 ? slots / tiles : 1, most = i8_dx_steps(rows) / 8;
+    if (splits > most) splits = most;
+    if (splits > 32) splits = 32;
+    if (splits < 1) splits = 1;
+    return I8DxPlan{shape, (int)splits, tiles};
+}
+
+// Where the parts of the gradients' workspace begin, and its size.
+struct I8BackwardSpace {
+    int64_t parts, sums, bytes;  // d_x parts, scale terms (bytes from the start); the coefficients come first
+};
+constexpr I8BackwardSpace i8_backward_space(int64_t rows, int64_t k, int64_t tokens, int type) {
+    const int64_t padded = ceil_of(rows, kI8ChannelPad) * kI8ChannelPad;
+    const int64_t coef = 4 * i8_limbs(type) * tokens * padded;
+    const I8DxPlan plan = i8_dx_plan(rows, k, tokens, type);
+    const int64_t dx = plan.splits > 1 ? 4 * plan.splits * tokens * k : 0;
+    const int64_t tiles = ceil_of(tokens, kI8Tiles[i8_tile_choice(rows, k, tokens, true)].tokens());
+    const int64_t parts = ceil_of(coef, 256) * 256, sums = parts + ceil_of(dx, 256) * 256;
+    return I8BackwardSpace{parts, sums, sums + 8 * rows * tiles};
+}
+constexpr int64_t gated_backward_workspace_bytes(int64_t rows, int64_t k, int64_t tokens, int type) {
+    return i8_backward_space(rows, k, tokens, type).bytes;
 }
 
 // Kernel launchers.  Arguments are already validated; geometry comes from

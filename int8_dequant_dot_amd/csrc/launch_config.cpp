@@ -174,11 +174,12 @@ int geo_i8_product(const int64_t *w, loom_launch_config *c) {
 }
 
 // i8_gated_projection_backward(rows, k, tokens): its first kernel, one
-// workgroup per 16 channels x 16 tokens.
+// workgroup per tile of i8_tile_choice.
 int geo_i8_backward(const int64_t *w, loom_launch_config *c) {
-    if (w[0] < 0 || w[1] < 0 || w[2] < 0) return LOOM_ERR_RANGE;
-    if (w[0] > 0 && ceil_div(w[2], 16) > kMaxGridWorkItems / ceil_div(w[0], 16)) return LOOM_ERR_RANGE;
-    return set(c, ceil_div(w[0], 16) * ceil_div(w[2], 16), 256, 0);
+    if (w[0] < 0 || w[1] < 0 || w[2] < 0 || w[0] > kI8BackwardMaxRows) return LOOM_ERR_RANGE;
+    // the second kernel's grid, of at least 32 tokens x 128 columns x 256 work-items a tile
+    if (ceil_div(w[2], 32) > kMaxGridWorkItems / 256 / (ceil_div(w[1], 128) + 1)) return LOOM_ERR_RANGE;
+    return geo_i8_tiles(w, true, c);
 }
 
 struct Export {
