@@ -119,6 +119,9 @@ def launch_config_invoke(token: int, workload) -> dict:
 
 # ------------------------------------------------------------------ tensor helpers
 
+# the current stream's handle without a Stream object around it (1.1 us a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 def _target(t: torch.Tensor, name: str):
     """The current HIP device index and its current stream: the C ABI launches
     there, so every tensor must live on that device.  ``t`` (the call's first
@@ -126,7 +129,7 @@ def _target(t: torch.Tensor, name: str):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     device = torch.cuda.current_device()
-    return device, torch.cuda.current_stream(device).cuda_stream
+    return device, _raw_stream(device)
 
 
 def _dev(t: torch.Tensor, dtype, name: str, device: int) -> torch.Tensor:
@@ -335,30 +338,55 @@ def _act(act: str) -> int:
 def _rows_of(t: torch.Tensor, dtype, rows: int, cols: int, name: str, device: int) -> int:
     """Checks a [rows][cols] matrix with unit column stride and any row stride >= cols; returns the row stride."""
     _dev(t, dtype, name, device)
-    _require(t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols,
-             f"{name} must be [{rows}][{cols}], got {list(t.shape)}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}][{cols}], got {list(t.shape)}")
     if rows == 0 or cols == 0:
         return max(cols, 1)
-    _require(cols == 1 or t.stride(1) == 1, f"{name} must have unit column stride")
+    stride, unit = t.stride()
+    if unit != 1 and cols != 1:
+        raise ValueError(f"{name} must have unit column stride")
     if rows == 1:
         return cols
-    _require(t.stride(0) >= cols, f"{name} has overlapping rows")
-    return t.stride(0)
+    if stride < cols:
+        raise ValueError(f"{name} has overlapping rows")
+    return stride
 
 
-def _product_operands(w, w_scale, x, x_scale, device, w_name="w", s_name="w_scale"):
-    """Checks packed weights [rows][k/4], activations [tokens][k/4] and their scales -> (rows, k, tokens, x)."""
+def _weights(w, w_scale, device, w_name, s_name):
+    """Checks packed weights [rows][k/4] and their scales -> (rows, k / 4)."""
     _dev(w, torch.int32, w_name, device)
-    _dev(x, torch.int32, "x", device)
-    if x.dim() == 1:
-        x = x.view(1, -1)
-    _require(w.dim() == 2 and w.is_contiguous(), f"{w_name} must be a contiguous [rows][k/4] tensor")
-    _require(x.dim() == 2 and x.is_contiguous() and x.shape[1] == w.shape[1],
-             f"x must be a contiguous [tokens][k/4] tensor with the same k as {w_name}")
+    if w.dim() != 2 or not w.is_contiguous():
+        raise ValueError(f"{w_name} must be a contiguous [rows][k/4] tensor")
     rows, kw = w.shape
     _buffer(w_scale, torch.float32, rows, s_name, device)
-    _buffer(x_scale, torch.float32, x.shape[0], "x_scale", device, optional=True)
-    return rows, 4 * kw, x.shape[0], x
+    return rows, kw
+
+
+def _activations(x, x_scale, kw, device, w_name):
+    """Checks packed activations [tokens][k/4] or [k/4] and their scales -> tokens."""
+    _dev(x, torch.int32, "x", device)
+    if x.dim() not in (1, 2) or not x.is_contiguous() or x.shape[-1] != kw:
+        raise ValueError(f"x must be a contiguous [tokens][k/4] tensor with the same k as {w_name}")
+    tokens = x.shape[0] if x.dim() == 2 else 1
+    _buffer(x_scale, torch.float32, tokens, "x_scale", device, optional=True)
+    return tokens
+
+
+def _gated_operands(w_gate, gate_scale, w_up, up_scale, x, x_scale, device):
+    """The operands of the gated projection -> (rows, k, tokens)."""
+    rows, kw = _weights(w_gate, gate_scale, device, "w_gate", "gate_scale")
+    _weights(w_up, up_scale, device, "w_up", "up_scale")
+    _require(w_up.shape == w_gate.shape, "w_up must be shaped as w_gate")
+    return rows, 4 * kw, _activations(x, x_scale, kw, device, "w_gate")
+
+
+def _result(out, dtype, tokens, rows, like, device):
+    """The output tensor (made here if None) -> (out, loom_type, row stride)."""
+    if out is None:
+        kind = _type(dtype, "dtype")
+        return torch.empty((tokens, rows), dtype=dtype, device=like.device), kind, rows
+    kind = _type(getattr(out, "dtype", None), "out")
+    return out, kind, _rows_of(out, out.dtype, tokens, rows, "out", device)
 
 
 def quantize_rows(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None):
@@ -386,17 +414,12 @@ def i8_matmul(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, x_scale: 
     """w int32 [rows][k/4], x int32 [tokens][k/4] or [k/4] (packed int8), w_scale f32 [rows], x_scale f32 [tokens],
     bias f32 [rows] -> out [tokens][rows] of ``dtype`` (or of ``out``, whose rows may be strided)."""
     device, stream = _target(w, "w")
-    rows, k, tokens, x = _product_operands(w, w_scale, x, x_scale, device)
+    rows, kw = _weights(w, w_scale, device, "w", "w_scale")
+    tokens = _activations(x, x_scale, kw, device, "w")
     _buffer(bias, torch.float32, rows, "bias", device, optional=True)
-    if out is None:
-        kind = _type(dtype, "dtype")
-        out = torch.empty(tokens, rows, dtype=dtype, device=w.device)
-        stride = rows
-    else:
-        kind = _type(getattr(out, "dtype", None), "out")
-        stride = _rows_of(out, out.dtype, tokens, rows, "out", device)
-    _check(_lib.loom_i8_matmul(_ptr(w), _ptr(w_scale), _ptr(x), _ptr(x_scale), _ptr(bias), rows, k, tokens, _ptr(out),
-                               kind, stride, stream), "i8_matmul")
+    out, kind, stride = _result(out, dtype, tokens, rows, w, device)
+    _check(_lib.loom_i8_matmul(_ptr(w), _ptr(w_scale), _ptr(x), _ptr(x_scale), _ptr(bias), rows, 4 * kw, tokens,
+                               _ptr(out), kind, stride, stream), "i8_matmul")
     return out
 
 
@@ -406,17 +429,9 @@ def i8_gated_projection(w_gate: torch.Tensor, gate_scale: torch.Tensor, w_up: to
     """act(x w_gate^T) * (x w_up^T) with the scales of i8_matmul -> out [tokens][rows] of ``dtype`` (or of ``out``).
     act: 'silu', 'gelu', 'gelu_tanh' or 'relu'."""
     device, stream = _target(w_gate, "w_gate")
-    rows, k, tokens, x = _product_operands(w_gate, gate_scale, x, x_scale, device, "w_gate", "gate_scale")
-    _product_operands(w_up, up_scale, x, x_scale, device, "w_up", "up_scale")
-    _require(w_up.shape == w_gate.shape, "w_up must be shaped as w_gate")
+    rows, k, tokens = _gated_operands(w_gate, gate_scale, w_up, up_scale, x, x_scale, device)
     code = _act(act)
-    if out is None:
-        kind = _type(dtype, "dtype")
-        out = torch.empty(tokens, rows, dtype=dtype, device=w_gate.device)
-        stride = rows
-    else:
-        kind = _type(getattr(out, "dtype", None), "out")
-        stride = _rows_of(out, out.dtype, tokens, rows, "out", device)
+    out, kind, stride = _result(out, dtype, tokens, rows, w_gate, device)
     _check(_lib.loom_i8_gated_projection(_ptr(w_gate), _ptr(gate_scale), _ptr(w_up), _ptr(up_scale), _ptr(x),
                                          _ptr(x_scale), rows, k, tokens, code, _ptr(out), kind, stride, stream),
            "i8_gated_projection")
@@ -441,9 +456,7 @@ def i8_gated_projection_backward(w_gate: torch.Tensor, gate_scale: torch.Tensor,
     d_x is the gradient of the dequantised activation x * x_scale.  A gradient that is not wanted is None.
     workspace: a uint8 buffer of i8_gated_projection_backward_workspace bytes, 16-byte aligned (made here if None)."""
     device, stream = _target(w_gate, "w_gate")
-    rows, k, tokens, x = _product_operands(w_gate, gate_scale, x, x_scale, device, "w_gate", "gate_scale")
-    _product_operands(w_up, up_scale, x, x_scale, device, "w_up", "up_scale")
-    _require(w_up.shape == w_gate.shape, "w_up must be shaped as w_gate")
+    rows, k, tokens = _gated_operands(w_gate, gate_scale, w_up, up_scale, x, x_scale, device)
     code = _act(act)
     kind = _type(getattr(d_out, "dtype", None), "d_out")
     stride = _rows_of(d_out, d_out.dtype, tokens, rows, "d_out", device)

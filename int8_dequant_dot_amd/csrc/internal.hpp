@@ -410,6 +410,17 @@ constexpr int64_t kMaxK = 131068;
 // its reciprocal could leave the f32 range, and its scale would be subnormal.
 constexpr float kQuantizeTiny = 0x1p-119f;
 
+// Waves of a row of the quantiser, by the registers that hold it (8 KiB of f32 a
+// wave): 1 (four rows a workgroup), 4, 8 or 16; with at most a row a CU, 16 from
+// 4096 columns, which is latency alone.  Rows past quantize_kept_columns are read twice.
+constexpr int kQuantizePacked = 4;
+constexpr int quantize_waves(int64_t rows, int64_t cols) {
+    if (cols <= 1024) return 1;
+    if (cols > 16384 || (rows <= 256 && cols >= 4096)) return 16;
+    return cols > 8192 ? 8 : 4;
+}
+constexpr int64_t quantize_kept_columns(int type) { return type == LOOM_F32 ? 32768 : 65536; }
+
 // The kernels of the int8 product and the gated projection.  Up to 8 tokens (16
 // for the product) stream the weights through registers (i8_stream_kernel: 16
 // weight rows a workgroup, 4 waves that split k); more go through LDS tiles of

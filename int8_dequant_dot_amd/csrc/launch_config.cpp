@@ -150,11 +150,15 @@ int geo_routed_combine(const int64_t *w, loom_launch_config *c) {
                 0);
 }
 
-// quantize_rows(rows, cols): one workgroup per row, each taking every
-// grid.x-th row once the grid reaches the work-item limit.
+// quantize_rows(rows, cols): one workgroup of quantize_waves per row, or per
+// kQuantizePacked rows of one wave each (LDS: the waves' maxima), each taking
+// every grid.x-th once the grid reaches the work-item limit.
 int geo_quantize_rows(const int64_t *w, loom_launch_config *c) {
     if (w[0] < 0 || w[1] < 0) return LOOM_ERR_RANGE;
-    return set(c, grid_stride_groups(w[0], 256), 256, 256 * 4);
+    const int waves = quantize_waves(w[0], w[1]);
+    const int64_t size = kSubgroupSize * (waves > 1 ? waves : kQuantizePacked);
+    return set(c, grid_stride_groups(waves > 1 ? w[0] : ceil_div(w[0], kQuantizePacked), size), (uint32_t)size,
+               4 * (uint32_t)waves);
 }
 
 // i8_matmul, i8_gated_projection (rows, k, tokens): few tokens take one
