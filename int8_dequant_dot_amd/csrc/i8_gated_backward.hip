@@ -50,7 +50,7 @@ struct Coefficients {
 // lanes of the same channels, then the waves, always in the same order.
 template <typename C, int LIMBS>
 __global__ __launch_bounds__(C::NW * kWave, 1) void coefficients_kernel(I8Product p, Coefficients o) {
-    typedef TileOut<C> Out;
+    typedef TileOut<C, true> Out;
     __shared__ __align__(1024) char lds[C::kLds];
     uint32_t ch, tok;
     tile_of(blockIdx.x, (p.rows + C::OUT_CH - 1) / C::OUT_CH, (p.tokens + C::TK - 1) / C::TK, 8, ch, tok);
@@ -71,11 +71,41 @@ __global__ __launch_bounds__(C::NW * kWave, 1) void coefficients_kernel(I8Produc
         ws[e] = p.w_scale[m];
         us[e] = p.up_scale[m];
     }
-    Out::each(loop, acc, [&](int64_t t, float xs, int4v a, int4v b) {
+    // four neighbours of d_out as they are in memory, for tokens t, t + by, .. (past
+    // the last, the last's)
+    const bool direct = whole && left >= 4;
+    auto fetch = [&](int count, int64_t t, int by, int4v (&into)[Out::PASSES]) {
+        const int64_t last = t - loop.lane / Out::LANES + count - 1;
+        if (o.type == LOOM_F32 && direct) {
+#pragma unroll
+            for (int i = 0; i < Out::PASSES; ++i)
+                into[i] = *(const int4v *)((const float *)o.d_out + min(t + i * by, last) * o.d_stride + n);
+        } else if (direct) {
+#pragma unroll
+            for (int i = 0; i < Out::PASSES; ++i) {
+                const uint2v v = *(const uint2v *)((const uint16_t *)o.d_out + min(t + i * by, last) * o.d_stride + n);
+                into[i] = int4v{(int)v.x, (int)v.y, 0, 0};
+            }
+        } else {
+            for (int i = 0; i < Out::PASSES; ++i) {
+                float d[4];
+                load4(o.d_out, o.type, min(t + i * by, last) * o.d_stride + n, left, false, d);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) into[i][e] = __builtin_bit_cast(int, d[e]);
+            }
+        }
+    };
+    Out::each(loop, acc, fetch, [&](int64_t t, float xs, int4v a, int4v b, int4v raw) {
         if (n >= o.padded) return;
         float d[4];
         uint32_t cg[4][LIMBS], cu[4][LIMBS];
-        load4(o.d_out, o.type, t * o.d_stride + n, left, whole, d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t w = (uint32_t)raw[e / 2] >> (16 * (e % 2));
+            if (o.type == LOOM_F32 || !direct) d[e] = __builtin_bit_cast(float, (int)raw[e]);
+            else if (o.type == LOOM_F16) d[e] = (float)__builtin_bit_cast(_Float16, (uint16_t)w);
+            else d[e] = __builtin_bit_cast(float, w << 16);
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float g = (float)a[e] * ws[e] * xs, u = (float)b[e] * us[e] * xs;

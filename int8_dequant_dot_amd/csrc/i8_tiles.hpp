@@ -325,29 +325,49 @@ struct TileLoop {
 // gated), n = out_channel(), the same for every call of a lane; tokens past the
 // end are left out.  Each wave moves its own part through its own piece of the
 // LDS, some token blocks at a time; the wide stores that follow are whole lines.
-template <typename C>
+//
+// FETCH: use gets 16 bytes that belong to the sums as well, with fetch(passes,
+// token of pass 0, tokens between passes, into) loading those of one lane for all
+// passes over some token blocks; they are loaded while the blocks before are in
+// use, and wait in LDS.
+template <typename C, bool FETCH = false>
 struct TileOut {
     static constexpr int OC = C::WT * 16 / (C::GATED ? 2 : 1);  // output channels of a wave
     static constexpr int LANES = OC / 4;                        // lanes of one token
     static constexpr int PER = kWave / LANES;                   // tokens of one pass
     static constexpr int ROW = C::WT * 64;                      // bytes of one token's sums in LDS
+    static constexpr int HELD = FETCH ? 16 * OC * 4 : 0;        // fetched bytes of a token block
     static constexpr int ROOM = C::kLds / C::NW;                // bytes of LDS a wave
-    static constexpr int FIT = (ROOM - 64 * C::XT) / (16 * ROW);
-    static constexpr int BLOCKS = FIT >= C::XT ? C::XT : FIT >= 4 && C::XT % 4 == 0 ? 4 : FIT >= 2 && C::XT % 2 == 0 ? 2 : 1;  // token blocks at a time
-    static_assert(C::XT % BLOCKS == 0 && LANES <= kWave && kWave % LANES == 0 && FIT > 0, "whole passes");
+    static constexpr int FIT = (ROOM - 64 * C::XT) / (16 * ROW + HELD);
+    // token blocks at a time
+    static constexpr int BLOCKS = FIT >= C::XT ? C::XT : FIT >= 4 && C::XT % 4 == 0 ? 4 : FIT >= 2 && C::XT % 2 == 0 ? 2 : 1;
+    static constexpr int PASSES = BLOCKS * 16 / PER;
+    static_assert(C::XT % BLOCKS == 0 && LANES <= kWave && kWave % LANES == 0 && FIT > 0 && PASSES > 0, "whole passes");
 
     template <typename Loop>
     static __device__ int64_t out_channel(const Loop &l) {
         return l.n0 + l.wm * OC + 4 * (l.lane % LANES);
     }
 
+    struct NoFetch {
+        __device__ void operator()(int, int64_t, int, int4v (&)[PASSES]) const {}
+    };
+
     template <typename Loop, typename Use>
     static __device__ __forceinline__ void each(const Loop &l, int4v (&acc)[C::WT][C::XT], Use &&use) {
+        each(l, acc, NoFetch{}, [&](int64_t t, float xs, int4v one, int4v two, int4v) { use(t, xs, one, two); });
+    }
+
+    template <typename Loop, typename Fetch, typename Use>
+    static __device__ __forceinline__ void each(const Loop &l, int4v (&acc)[C::WT][C::XT], Fetch &&fetch, Use &&use) {
         char *mine = l.lds + l.wave * ROOM;
         float *scales = (float *)(mine + ROOM - 64 * C::XT);
-        const int m = l.lane & 15, g = l.lane >> 4, c = l.lane % LANES;
+        int4v *held = (int4v *)(mine + BLOCKS * 16 * ROW) + l.lane;
+        const int m = l.lane & 15, g = l.lane >> 4, c = l.lane % LANES, r0 = l.lane / LANES;
         const int64_t first = l.t0 + l.wn * C::XT * 16;
         const int count = (int)min((int64_t)C::XT * 16, l.p.tokens - first);
+        int4v next[PASSES];
+        if (FETCH && count > 0) fetch(count, first + r0, PER, next);
         __syncthreads();  // every wave is done with the tile
         for (int i = l.lane; i < count; i += kWave) scales[i] = l.p.x_scale ? l.p.x_scale[first + i] : 1.0f;
         each_index<C::XT / BLOCKS>([&](auto round) {
@@ -358,15 +378,22 @@ struct TileOut {
 #pragma unroll
                 for (int i = 0; i < C::WT; ++i)
                     *(int4v *)(mine + (x * 16 + m) * ROW + (((i * 4 + g) ^ (m & 7)) << 4)) = acc[i][b + x];
+            if constexpr (FETCH) {
+#pragma unroll
+                for (int i = 0; i < PASSES; ++i) held[i * kWave] = next[i];
+                if (b + BLOCKS < C::XT && count > (b + BLOCKS) * 16)
+                    fetch(count - (b + BLOCKS) * 16, first + (b + BLOCKS) * 16 + r0, PER, next);
+            }
             wait_lds();
 #pragma unroll 2
-            for (int r = l.lane / LANES; r < BLOCKS * 16; r += PER) {
+            for (int r = r0; r < BLOCKS * 16; r += PER) {
                 if (b * 16 + r >= count) break;
                 const char *row = mine + r * ROW;
                 const int4v one = *(const int4v *)(row + ((c ^ (r & 7)) << 4));
-                int4v two = one;
+                int4v two = one, more = one;
                 if constexpr (C::GATED) two = *(const int4v *)(row + (((c + LANES) ^ (r & 7)) << 4));
-                use(first + b * 16 + r, scales[b * 16 + r], one, two);
+                if constexpr (FETCH) more = held[r / PER * kWave];
+                use(first + b * 16 + r, scales[b * 16 + r], one, two, more);
             }
             wait_lds();
         });

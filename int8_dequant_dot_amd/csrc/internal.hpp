@@ -525,7 +525,7 @@ struct I8DxShape {
     }
     constexpr int resident(int limbs) const { return 160 * 1024 / (ring(limbs) * step_bytes(limbs)); }
 };
-constexpr I8DxShape kI8Dx[] = {{2, 2, 8, 8}, {2, 2, 4, 4}, {4, 1, 2, 2}};
+constexpr I8DxShape kI8Dx[] = {{4, 1, 4, 16}, {2, 2, 4, 4}, {4, 1, 2, 2}};
 struct I8DxPlan {
     int shape, splits;
     int64_t tiles;
