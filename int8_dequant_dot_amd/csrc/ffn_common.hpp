@@ -37,6 +37,31 @@ __device__ __forceinline__ void store4(void *out, int type, int64_t at, int64_t 
     else if (type == LOOM_F16) store4_as((_Float16 *)out + at, left, whole, y);
     else store4_as((__bf16 *)out + at, left, whole, y);
 }
+// Four neighbours of each of N places `by` elements apart, where live: one branch
+// on the type and on the row's alignment for all of them.
+template <typename T, int N>
+__device__ __forceinline__ void store4_each_as(T *to, int64_t by, int64_t left, bool whole, const bool (&live)[N],
+                                               const float (&y)[N][4]) {
+    if (whole && left >= 4) {
+        typedef T V __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (live[j]) *(V *)(to + j * by) = V{(T)y[j][0], (T)y[j][1], (T)y[j][2], (T)y[j][3]};
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (live[j] && e < left) to[j * by + e] = (T)y[j][e];
+    }
+}
+template <int N>
+__device__ __forceinline__ void store4_each(void *out, int type, int64_t at, int64_t by, int64_t left, bool whole,
+                                            const bool (&live)[N], const float (&y)[N][4]) {
+    if (type == LOOM_F32) store4_each_as((float *)out + at, by, left, whole, live, y);
+    else if (type == LOOM_F16) store4_each_as((_Float16 *)out + at, by, left, whole, live, y);
+    else store4_each_as((__bf16 *)out + at, by, left, whole, live, y);
+}
 __device__ __forceinline__ float load1(const void *in, int type, int64_t at) {
     if (type == LOOM_F32) return ((const float *)in)[at];
     if (type == LOOM_F16) return (float)((const _Float16 *)in)[at];
@@ -95,6 +120,19 @@ __device__ __forceinline__ float act_value(int act, float g) {
         case LOOM_GELU: return g * normal_cdf(g);
         case LOOM_GELU_TANH: return g * tanh_form_cdf(tanh_form_gate(g));
         default: return g < 0.0f ? 0.0f : g;
+    }
+}
+
+// body with the activation as a compile-time constant: one branch for all that
+// body computes.
+template <int ACT> struct Activation { static constexpr int value = ACT; };
+template <typename Body>
+__device__ __forceinline__ void with_activation(int act, Body &&body) {
+    switch (act) {
+        case LOOM_SILU: return body(Activation<LOOM_SILU>{});
+        case LOOM_GELU: return body(Activation<LOOM_GELU>{});
+        case LOOM_GELU_TANH: return body(Activation<LOOM_GELU_TANH>{});
+        default: return body(Activation<LOOM_RELU>{});
     }
 }
 

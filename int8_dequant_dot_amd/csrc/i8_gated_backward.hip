@@ -71,58 +71,72 @@ __global__ __launch_bounds__(C::NW * kWave, 1) void coefficients_kernel(I8Produc
         ws[e] = p.w_scale[m];
         us[e] = p.up_scale[m];
     }
-    // four neighbours of d_out as they are in memory, for tokens t, t + by, .. (past
-    // the last, the last's)
+    // four neighbours of d_out as they are in memory (past the last token, its)
     const bool direct = whole && left >= 4;
-    auto fetch = [&](int count, int64_t t, int by, int4v (&into)[Out::PASSES]) {
-        const int64_t last = t - loop.lane / Out::LANES + count - 1;
+    const int64_t t1 = Out::first_token(loop);
+    auto fetch = [&](int pass, int4v (&into)[Out::PASSES]) {
+        const int64_t t = t1 + pass * Out::PER, last = p.tokens - 1;
         if (o.type == LOOM_F32 && direct) {
 #pragma unroll
             for (int i = 0; i < Out::PASSES; ++i)
-                into[i] = *(const int4v *)((const float *)o.d_out + min(t + i * by, last) * o.d_stride + n);
+                into[i] = *(const int4v *)((const float *)o.d_out + min(t + i * Out::PER, last) * o.d_stride + n);
         } else if (direct) {
 #pragma unroll
             for (int i = 0; i < Out::PASSES; ++i) {
-                const uint2v v = *(const uint2v *)((const uint16_t *)o.d_out + min(t + i * by, last) * o.d_stride + n);
+                const uint2v v =
+                    *(const uint2v *)((const uint16_t *)o.d_out + min(t + i * Out::PER, last) * o.d_stride + n);
                 into[i] = int4v{(int)v.x, (int)v.y, 0, 0};
             }
         } else {
+#pragma unroll
             for (int i = 0; i < Out::PASSES; ++i) {
                 float d[4];
-                load4(o.d_out, o.type, min(t + i * by, last) * o.d_stride + n, left, false, d);
+                load4(o.d_out, o.type, min(t + i * Out::PER, last) * o.d_stride + n, left, false, d);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) into[i][e] = __builtin_bit_cast(int, d[e]);
             }
         }
     };
-    Out::each(loop, acc, fetch, [&](int64_t t, float xs, int4v a, int4v b, int4v raw) {
+    const int64_t start = t1 * 2 * o.padded + n, by = Out::PER * 2 * o.padded, limb = (int64_t)p.tokens * 2 * o.padded;
+    Out::each(loop, acc, fetch, [&](const typename Out::Pass (&pass)[Out::GROUP]) {
         if (n >= o.padded) return;
-        float d[4];
-        uint32_t cg[4][LIMBS], cu[4][LIMBS];
+        float cg[Out::GROUP][4], cu[Out::GROUP][4];
+        with_activation(p.act, [&](auto act) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t w = (uint32_t)raw[e / 2] >> (16 * (e % 2));
-            if (o.type == LOOM_F32 || !direct) d[e] = __builtin_bit_cast(float, (int)raw[e]);
-            else if (o.type == LOOM_F16) d[e] = (float)__builtin_bit_cast(_Float16, (uint16_t)w);
-            else d[e] = __builtin_bit_cast(float, w << 16);
-        }
+            for (int j = 0; j < Out::GROUP; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float g = (float)a[e] * ws[e] * xs, u = (float)b[e] * us[e] * xs;
-            float value, slope;
-            act_value_slope(p.act, g, value, slope);
-            const float dg = e < left ? d[e] * u * slope : 0.0f, du = e < left ? d[e] * value : 0.0f;
-            tg[e] = tg[e] + dg * ((float)a[e] * xs);
-            tu[e] = tu[e] + du * ((float)b[e] * xs);
-            limbs_of<LIMBS>(e < left ? dg * ws[e] : 0.0f, cg[e]);
-            limbs_of<LIMBS>(e < left ? du * us[e] : 0.0f, cu[e]);
-        }
-        if (o.coef) {
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t w = (uint32_t)pass[j].more[e / 2] >> (16 * (e % 2));
+                    const float d = o.type == LOOM_F32 || !direct ? __builtin_bit_cast(float, (int)pass[j].more[e])
+                                    : o.type == LOOM_F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)w)
+                                                         : __builtin_bit_cast(float, w << 16);
+                    const float a = (float)pass[j].one[e], b = (float)pass[j].two[e], xs = pass[j].scale;
+                    const float g = a * ws[e] * xs, u = b * us[e] * xs;
+                    float value, slope;
+                    act_value_slope(decltype(act)::value, g, value, slope);
+                    const bool in = pass[j].live && e < left;
+                    const float dg = in ? d * u * slope : 0.0f, du = in ? d * value : 0.0f;
+                    tg[e] = tg[e] + (in ? dg * (a * xs) : 0.0f);
+                    tu[e] = tu[e] + (in ? du * (b * xs) : 0.0f);
+                    cg[j][e] = dg * ws[e];
+                    cu[j][e] = du * us[e];
+                }
+        });
+        if (!o.coef) return;
+#pragma unroll
+        for (int j = 0; j < Out::GROUP; ++j) {
+            uint32_t lg[4][LIMBS], lu[4][LIMBS];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                limbs_of<LIMBS>(e < left ? cg[j][e] : 0.0f, lg[e]);
+                limbs_of<LIMBS>(e < left ? cu[j][e] : 0.0f, lu[e]);
+            }
+            if (!pass[j].live) continue;
 #pragma unroll
             for (int i = 0; i < LIMBS; ++i) {
-                uint16_t *row = o.coef + ((int64_t)i * p.tokens + t) * 2 * o.padded + n;
-                *(uint2v *)row = uint2v{cg[0][i] | cg[1][i] << 16, cg[2][i] | cg[3][i] << 16};
-                *(uint2v *)(row + o.padded) = uint2v{cu[0][i] | cu[1][i] << 16, cu[2][i] | cu[3][i] << 16};
+                uint16_t *row = o.coef + start + (pass[0].i + j) * by + i * limb;
+                *(uint2v *)row = uint2v{lg[0][i] | lg[1][i] << 16, lg[2][i] | lg[3][i] << 16};
+                *(uint2v *)(row + o.padded) = uint2v{lu[0][i] | lu[1][i] << 16, lu[2][i] | lu[3][i] << 16};
             }
         }
     });
@@ -393,12 +407,18 @@ __global__ __launch_bounds__(C::NW * kWave, 1) void d_x_kernel(I8Product p, DxOp
     void *out = parts ? (void *)((float *)o.out + (int64_t)blockIdx.y * p.tokens * o.k) : o.out;
     const bool whole = o.k % 4 == 0 && (uintptr_t)out % (4 * element_bytes(type)) == 0;
     const int64_t n = TileOut<C>::out_channel(loop), left = o.k - n;
-    TileOut<C>::each(loop, acc, [&](int64_t t, float, int4v a, int4v) {
-        if (left <= 0) return;
-        float y[4];
+    typedef TileOut<C> Out;
+    const int64_t start = Out::first_token(loop) * o.k + n, by = Out::PER * o.k;
+    Out::each(loop, acc, [&](const typename Out::Pass (&pass)[Out::GROUP]) {
+        float y[Out::GROUP][4];
+        bool live[Out::GROUP];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = __builtin_bit_cast(float, (int)a[e]);
-        store4(out, type, t * o.k + n, left, whole, y);
+        for (int j = 0; j < Out::GROUP; ++j) {
+            live[j] = pass[j].live;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[j][e] = __builtin_bit_cast(float, (int)pass[j].one[e]);
+        }
+        store4_each(out, type, start + pass[0].i * by, by, left, whole, live, y);
     });
 }
 

@@ -154,16 +154,33 @@ __global__ __launch_bounds__(C::NW * kWave, 1) void i8_tile_kernel(I8Product p, 
         us[e] = C::GATED ? p.up_scale[m] : 1.0f;
         bias[e] = !C::GATED && p.bias ? p.bias[m] : 0.0f;
     }
-    TileOut<C>::each(loop, acc, [&](int64_t t, float xs, int4v a, int4v u) {
-        if (left <= 0) return;
-        float y[4];
+    typedef TileOut<C> Out;
+    const int64_t start = Out::first_token(loop) * p.out_stride + n, by = Out::PER * p.out_stride;
+    Out::each(loop, acc, [&](const typename Out::Pass (&pass)[Out::GROUP]) {
+        float y[Out::GROUP][4];
+        bool live[Out::GROUP];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            y[e] = (float)a[e] * ws[e] * xs;
-            if constexpr (C::GATED) y[e] = act_value(p.act, y[e]) * ((float)u[e] * us[e] * xs);
-            else if (p.bias) y[e] = y[e] + bias[e];
+        for (int j = 0; j < Out::GROUP; ++j) {
+            live[j] = pass[j].live;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[j][e] = (float)pass[j].one[e] * ws[e] * pass[j].scale;
         }
-        store4(p.out, type, t * p.out_stride + n, left, whole, y);
+        if constexpr (C::GATED) {
+            with_activation(p.act, [&](auto act) {
+#pragma unroll
+                for (int j = 0; j < Out::GROUP; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[j][e] = act_value(decltype(act)::value, y[j][e]) *
+                                  ((float)pass[j].two[e] * us[e] * pass[j].scale);
+            });
+        } else if (p.bias) {
+#pragma unroll
+            for (int j = 0; j < Out::GROUP; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[j][e] = y[j][e] + bias[e];
+        }
+        store4_each(p.out, type, start + pass[0].i * by, by, left, whole, live, y);
     });
 }
 

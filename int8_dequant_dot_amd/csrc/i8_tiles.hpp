@@ -320,16 +320,18 @@ struct TileLoop {
 };
 
 // Hands the tile's sums to `use`, transposed through LDS so that a lane holds
-// four neighbouring channels and the lanes beside it the channels beside those:
-// use(token, its scale, acc) with acc of channels n .. n + 3 (and their up sums,
-// gated), n = out_channel(), the same for every call of a lane; tokens past the
-// end are left out.  Each wave moves its own part through its own piece of the
-// LDS, some token blocks at a time; the wide stores that follow are whole lines.
+// four neighbouring channels n .. n + 3 of one token (and their up sums, gated),
+// n = out_channel(), the same for every pass of a lane, and the lanes beside it the
+// channels beside those.  use gets GROUP passes at once, pass i token
+// first_token() + i * PER, so that their reads, arithmetic and stores overlap and
+// it branches on types and activations once for all of them; passes that are not
+// live are past the last token.  Each wave moves its own part through its own
+// piece of the LDS, some token blocks at a time; wide stores are whole lines.
+// (One pass at a time took 23 us of a 256 x 256 tile.)
 //
-// FETCH: use gets 16 bytes that belong to the sums as well, with fetch(passes,
-// token of pass 0, tokens between passes, into) loading those of one lane for all
-// passes over some token blocks; they are loaded while the blocks before are in
-// use, and wait in LDS.
+// FETCH: a pass also gets 16 bytes that belong to its sums, with fetch(first pass,
+// into) loading those of one lane for PASSES passes; they are loaded while the
+// blocks before are in use, and wait in LDS.
 template <typename C, bool FETCH = false>
 struct TileOut {
     static constexpr int OC = C::WT * 16 / (C::GATED ? 2 : 1);  // output channels of a wave
@@ -349,13 +351,22 @@ struct TileOut {
         return l.n0 + l.wm * OC + 4 * (l.lane % LANES);
     }
 
-    struct NoFetch {
-        __device__ void operator()(int, int64_t, int, int4v (&)[PASSES]) const {}
+    template <typename Loop>
+    static __device__ int64_t first_token(const Loop &l) {
+        return l.t0 + l.wn * C::XT * 16 + l.lane / LANES;
+    }
+
+    static constexpr int GROUP = PASSES % 4 == 0 ? 4 : PASSES % 2 == 0 ? 2 : 1;
+    struct Pass {
+        int i;          // the same in every lane
+        bool live;
+        float scale;    // the token's
+        int4v one, two, more;
     };
 
     template <typename Loop, typename Use>
     static __device__ __forceinline__ void each(const Loop &l, int4v (&acc)[C::WT][C::XT], Use &&use) {
-        each(l, acc, NoFetch{}, [&](int64_t t, float xs, int4v one, int4v two, int4v) { use(t, xs, one, two); });
+        each(l, acc, [](int, int4v (&)[PASSES]) {}, use);
     }
 
     template <typename Loop, typename Fetch, typename Use>
@@ -367,11 +378,12 @@ struct TileOut {
         const int64_t first = l.t0 + l.wn * C::XT * 16;
         const int count = (int)min((int64_t)C::XT * 16, l.p.tokens - first);
         int4v next[PASSES];
-        if (FETCH && count > 0) fetch(count, first + r0, PER, next);
+        if (FETCH && count > 0) fetch(0, next);
         __syncthreads();  // every wave is done with the tile
         for (int i = l.lane; i < count; i += kWave) scales[i] = l.p.x_scale ? l.p.x_scale[first + i] : 1.0f;
         each_index<C::XT / BLOCKS>([&](auto round) {
             constexpr int b = decltype(round)::value * BLOCKS;
+            if (count <= b * 16) return;
             keep<b>(acc);
 #pragma unroll
             for (int x = 0; x < BLOCKS; ++x)
@@ -381,19 +393,24 @@ struct TileOut {
             if constexpr (FETCH) {
 #pragma unroll
                 for (int i = 0; i < PASSES; ++i) held[i * kWave] = next[i];
-                if (b + BLOCKS < C::XT && count > (b + BLOCKS) * 16)
-                    fetch(count - (b + BLOCKS) * 16, first + (b + BLOCKS) * 16 + r0, PER, next);
+                if (b + BLOCKS < C::XT && count > (b + BLOCKS) * 16) fetch((b + BLOCKS) * 16 / PER, next);
             }
             wait_lds();
-#pragma unroll 2
-            for (int r = r0; r < BLOCKS * 16; r += PER) {
-                if (b * 16 + r >= count) break;
-                const char *row = mine + r * ROW;
-                const int4v one = *(const int4v *)(row + ((c ^ (r & 7)) << 4));
-                int4v two = one, more = one;
-                if constexpr (C::GATED) two = *(const int4v *)(row + (((c + LANES) ^ (r & 7)) << 4));
-                if constexpr (FETCH) more = held[r / PER * kWave];
-                use(first + b * 16 + r, scales[b * 16 + r], one, two, more);
+#pragma unroll 1
+            for (int at = 0; at < PASSES; at += GROUP) {
+                Pass pass[GROUP];
+#pragma unroll
+                for (int j = 0; j < GROUP; ++j) {
+                    const int r = r0 + (at + j) * PER;
+                    const char *row = mine + r * ROW;
+                    pass[j].i = b * 16 / PER + at + j;
+                    pass[j].live = b * 16 + r < count;
+                    pass[j].scale = scales[b * 16 + r];
+                    pass[j].one = *(const int4v *)(row + ((c ^ (r & 7)) << 4));
+                    if constexpr (C::GATED) pass[j].two = *(const int4v *)(row + (((c + LANES) ^ (r & 7)) << 4));
+                    if constexpr (FETCH) pass[j].more = held[(at + j) * kWave];
+                }
+                use(pass);
             }
             wait_lds();
         });
