@@ -42,7 +42,9 @@ struct Coefficients {
     int type;
     uint16_t *coef;  // [limbs][tokens][2][padded], or NULL
     int64_t padded;
-    float *sums;     // [token tiles][2][rows], or NULL
+    float *sums;     // [token tiles][2][rows]
+    float *scale[2]; // one token tile: the scale gradients themselves, or NULL
+    bool whole_sums; // there is one token tile
 };
 
 // Both products again, then d_x's coefficients and the tile's terms of the scale
@@ -150,7 +152,7 @@ __global__ __launch_bounds__(C::NW * kWave, 1) void coefficients_kernel(I8Produc
             ((uint32_t *)at)[i % words] = 0;
         }
     }
-    if (!o.sums) return;
+    if (!o.sums && !o.scale[0] && !o.scale[1]) return;
     __syncthreads();
     // [waves][2][OC] sums
     float *mine = (float *)lds + loop.wave * 2 * Out::OC;
@@ -174,7 +176,8 @@ __global__ __launch_bounds__(C::NW * kWave, 1) void coefficients_kernel(I8Produc
 #pragma unroll
         for (int wn = 0; wn < C::WN; ++wn)
             sum = sum + ((const float *)lds)[((wn * C::WM + wm) * 2 + which) * Out::OC + c % Out::OC];
-        o.sums[((int64_t)tok * 2 + which) * p.rows + loop.n0 + c] = sum;
+        if (!o.whole_sums) o.sums[((int64_t)tok * 2 + which) * p.rows + loop.n0 + c] = sum;
+        else if (o.scale[which]) o.scale[which][loop.n0 + c] = sum;
     }
 }
 
@@ -427,7 +430,15 @@ __global__ __launch_bounds__(256) void add_parts_kernel(const float *__restrict_
     // count is a multiple of 4
     for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < count; i += (int64_t)gridDim.x * 1024) {
         float4v sum = *(const float4v *)(parts + i);
-        for (int s = 1; s < splits; ++s) sum = sum + *(const float4v *)(parts + s * count + i);
+        int s = 1;
+        for (; s + 8 <= splits; s += 8) {  // eight loads in flight, added in order
+            float4v part[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) part[j] = *(const float4v *)(parts + (s + j) * count + i);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = sum + part[j];
+        }
+        for (; s < splits; ++s) sum = sum + *(const float4v *)(parts + s * count + i);
         const float y[4] = {sum[0], sum[1], sum[2], sum[3]};
         store4(d_x, type, i, 4, whole, y);
     }
@@ -464,11 +475,13 @@ hipError_t run(const loom_launch_config &cfg, const I8Product &p, const void *d_
     const bool scales = (d_gate || d_up) && rows > 0, inputs = d_x && tokens > 0 && k > 0;
     uint16_t *coef = inputs ? (uint16_t *)workspace : nullptr;
     float *sums = scales ? (float *)((char *)workspace + space.sums) : nullptr;
+    const bool one = tokens > 0 && tokens <= kI8Tiles[shape].tokens();
     if (tokens > 0 && rows > 0) {
-        const Coefficients o = {d_out, d_stride, type, coef, padded, sums};
+        const Coefficients o = {d_out, d_stride, type, coef, padded, one ? nullptr : sums,
+                                {one ? d_gate : nullptr, one ? d_up : nullptr}, one};
         launch_coefficients<LIMBS>(shape, dim3(cfg.workgroups[0]), dim3(cfg.workgroup_size[0]), p, o, stream);
     }
-    if (scales)
+    if (scales && !one)
         hipLaunchKernelGGL(scale_gradients_kernel, dim3((uint32_t)((2 * rows + 255) / 256)), dim3(256), 0, stream,
                            sums, ceil_of(tokens, kI8Tiles[shape].tokens()), rows, d_gate, d_up);
     if (!inputs) return hipGetLastError();
@@ -485,12 +498,13 @@ hipError_t run(const loom_launch_config &cfg, const I8Product &p, const void *d_
     plain.x_scale = nullptr;  // the tile's output applies it
     const DxOperands o = {{(const int8_t *)p.w, (const int8_t *)p.w_up}, coef, padded, rows, k, plan.splits,
                           plan.splits > 1 ? (void *)parts : d_x, type};
-    if (plan.shape == 0) {
-        if constexpr (LIMBS == 1) launch_d_x<0, LIMBS>(plan, plain, o, stream);
-    } else if (plan.shape == 1) {
-        launch_d_x<1, LIMBS>(plan, plain, o, stream);
-    } else {
-        launch_d_x<2, LIMBS>(plan, plain, o, stream);
+    switch (plan.shape) {
+        case 0:
+            if constexpr (LIMBS == 1) launch_d_x<0, LIMBS>(plan, plain, o, stream);
+            break;
+        case 1: launch_d_x<1, LIMBS>(plan, plain, o, stream); break;
+        case 2: launch_d_x<2, LIMBS>(plan, plain, o, stream); break;
+        default: launch_d_x<3, LIMBS>(plan, plain, o, stream);
     }
     if (plan.splits > 1)
         hipLaunchKernelGGL(add_parts_kernel, flat, dim3(256), 0, stream, parts, plan.splits, count, d_x, type, whole);

@@ -525,24 +525,48 @@ struct I8DxShape {
     }
     constexpr int resident(int limbs) const { return 160 * 1024 / (ring(limbs) * step_bytes(limbs)); }
 };
-constexpr I8DxShape kI8Dx[] = {{4, 1, 4, 16}, {2, 2, 4, 4}, {4, 1, 2, 2}};
+constexpr I8DxShape kI8Dx[] = {{4, 1, 4, 16}, {2, 2, 4, 4}, {4, 1, 2, 2}, {4, 1, 4, 8}};
+constexpr int kI8DxCount = 4;
 struct I8DxPlan {
     int shape, splits;
     int64_t tiles;
 };
 constexpr int64_t i8_dx_steps(int64_t rows) { return 2 * ceil_of(rows, kI8ChannelPad); }
+
+// The shape and the number of parts with the least estimated time, as
+// i8_tile_choice estimates it: a step of r workgroups a CU takes the longest of
+// 0.4 us (0.3 for the smallest shape), its bytes at 58 KB/us and its products at 7 M operations/us (the
+// conversions of the weights included); parts cost their traffic at 5 TB/s and a
+// launch.  The 256-token shape is for one limb: its LDS holds no ring of more.
 constexpr I8DxPlan i8_dx_plan(int64_t rows, int64_t k, int64_t tokens, int type) {
     const int limbs = i8_limbs(type);
-    int shape = tokens <= 32 ? 2 : 1;
-    if (limbs == 1 && ceil_of(k, 256) * ceil_of(tokens, 256) >= 160) shape = 0;
-    const I8DxShape &s = kI8Dx[shape];
-    const int64_t tiles = ceil_of(k, s.columns()) * ceil_of(tokens, s.tokens());
-    const int64_t slots = 256 * s.resident(limbs);
-    int64_t splits = tiles > 0 ? slots / tiles : 1, most = i8_dx_steps(rows) / 8;
-    if (splits > most) splits = most;
-    if (splits > 32) splits = 32;
-    if (splits < 1) splits = 1;
-    return I8DxPlan{shape, (int)splits, tiles};
+    I8DxPlan best{2, 1, 0};
+    double best_us = -1;
+    for (int i = limbs == 1 ? 0 : 1; i < kI8DxCount; ++i) {
+        const I8DxShape &t = kI8Dx[i];
+        const int64_t tiles = ceil_of(k, t.columns()) * ceil_of(tokens, t.tokens()), round = 256 * t.resident(limbs);
+        for (int splits = 1; splits <= 32; splits = splits < 4 ? splits + 1 : splits * 3 / 2) {
+            const int64_t steps = ceil_of(i8_dx_steps(rows), splits), all = tiles * splits;
+            if (splits > 1 && steps < 8) break;
+            double us = splits > 1 ? 4 + 8.0 * splits * (double)tokens * (double)k / 5e6 : 0;
+            const int64_t full = all / round, rest = ceil_of(all % round, 256);
+            for (int last = 0; last < 2; ++last) {
+                const double r = last ? (double)rest : (double)t.resident(limbs);
+                const double times = last ? (rest > 0) : (double)full;
+                double step = i == 2 ? 0.3 : 0.4;
+                const double load = r * t.step_bytes(limbs) / 58e3;
+                const double math = r * t.columns() * t.tokens() * 128.0 * limbs / 7e6;
+                if (load > step) step = load;
+                if (math > step) step = math;
+                us += times * (step * (double)steps + 3);
+            }
+            if (best_us < 0 || us < best_us) {
+                best = I8DxPlan{i, splits, tiles};
+                best_us = us;
+            }
+        }
+    }
+    return best;
 }
 
 // Where the parts of the gradients' workspace begin, and its size.
