@@ -63,7 +63,7 @@ __global__ __launch_bounds__(C::NW * kWave, 1) void coefficients_kernel(I8Produc
 #pragma unroll
         for (int x = 0; x < C::XT; ++x) acc[i][x] = int4v{0, 0, 0, 0};
     const int steps = p.kw / 32;
-    loop.run(acc, p.tokens <= C::TK && steps > 0 ? (int)(ch * 5 % steps) : 0);
+    loop.run(acc, 0, steps, p.tokens <= C::TK && steps > 0 ? (int)(ch * 5 % steps) : 0, p.kw % 32 != 0);
     const bool whole = o.d_stride % 4 == 0 && (uintptr_t)o.d_out % (4 * element_bytes(o.type)) == 0;
     const int64_t n = Out::out_channel(loop), left = p.rows - n;
     float ws[4], us[4], tg[4] = {}, tu[4] = {};
@@ -470,7 +470,7 @@ hipError_t run(const loom_launch_config &cfg, const I8Product &p, const void *d_
                void *d_x, float *d_gate, float *d_up, void *workspace, hipStream_t stream) {
     const int64_t rows = p.rows, tokens = p.tokens, k = 4 * (int64_t)p.kw;
     const I8BackwardSpace space = i8_backward_space(rows, k, tokens, type);
-    const int shape = i8_tile_choice(rows, k, tokens, true);
+    const int shape = i8_tile_choice(rows, k, tokens, true, false);
     const int64_t padded = ceil_of(rows, kI8ChannelPad) * kI8ChannelPad;
     const bool scales = (d_gate || d_up) && rows > 0, inputs = d_x && tokens > 0 && k > 0;
     uint16_t *coef = inputs ? (uint16_t *)workspace : nullptr;

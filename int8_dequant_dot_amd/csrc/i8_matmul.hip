@@ -143,7 +143,7 @@ __global__ __launch_bounds__(C::NW * kWave, 1) void i8_tile_kernel(I8Product p, 
 #pragma unroll
         for (int x = 0; x < C::XT; ++x) acc[i][x] = int4v{};
     const int steps = p.kw / 32;
-    loop.run(acc, p.tokens <= C::TK && steps > 0 ? (int)(ch * 5 % steps) : 0);
+    loop.run(acc, 0, steps, p.tokens <= C::TK && steps > 0 ? (int)(ch * 5 % steps) : 0, p.kw % 32 != 0);
     const bool whole = p.out_stride % 4 == 0 && (uintptr_t)p.out % (4 * element_bytes(type)) == 0;
     const int64_t n = TileOut<C>::out_channel(loop), left = p.rows - n;
     float ws[4], us[4], bias[4];
@@ -184,11 +184,72 @@ __global__ __launch_bounds__(C::NW * kWave, 1) void i8_tile_kernel(I8Product p, 
     });
 }
 
+// Few tiles: the waves of a workgroup split k, each running its own tile loop over
+// its own rings with no barrier, and add their sums at the end.  A CU then has four
+// chains of loads in flight instead of one: 32 tokens x 500 channels x k 16000
+// took 22 us with the tile shared by the waves, 11 us so.
+template <typename C>
+__global__ __launch_bounds__(C::kShape.waves() * kWave, 1) void i8_split_kernel(I8Product p, int type) {
+    constexpr int S = C::kShape.split, ROW = C::CH * 4;  // bytes of a token's sums
+    static_assert(C::CH == 32 && C::kLds >= C::TK * ROW, "the sums fit the rings");
+    __shared__ __align__(1024) char lds[S * C::kLds];
+    uint32_t ch, tok;
+    tile_of(blockIdx.x, (p.rows + C::OUT_CH - 1) / C::OUT_CH, (p.tokens + C::TK - 1) / C::TK, 8, ch, tok);
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave)), lane = lane_id();
+    TileLoop<C> loop(p, lds + wave * C::kLds, (int64_t)ch * C::OUT_CH, (int64_t)tok * C::TK);
+    int4v acc[C::WT][C::XT];
+#pragma unroll
+    for (int i = 0; i < C::WT; ++i)
+#pragma unroll
+        for (int x = 0; x < C::XT; ++x) acc[i][x] = int4v{0, 0, 0, 0};
+    const int all = p.kw / 32, begin = (int)((int64_t)all * wave / S), end = (int)((int64_t)all * (wave + 1) / S);
+    loop.run(acc, begin, end - begin, end > begin ? (int)(ch * 5 % (end - begin)) : 0, wave == S - 1 && p.kw % 32 != 0);
+    // the sums of token t, chunks of four channels, at chunk c ^ (t & 7) of its row
+#pragma unroll
+    for (int i = 0; i < C::WT; ++i)
+#pragma unroll
+        for (int x = 0; x < C::XT; ++x) {
+            const int t = x * 16 + (lane & 15);
+            *(int4v *)(loop.lds + t * ROW + (((i * 4 + (lane >> 4)) ^ (t & 7)) << 4)) = acc[i][x];
+        }
+    __syncthreads();
+    constexpr int LANES = C::OUT_CH / 4;
+    const bool whole = p.out_stride % 4 == 0 && (uintptr_t)p.out % (4 * element_bytes(type)) == 0;
+    for (int o = threadIdx.x; o < C::TK * LANES; o += S * kWave) {
+        const int t = o / LANES, c = o % LANES;
+        const int64_t n = loop.n0 + 4 * c, left = p.rows - n, token = loop.t0 + t;
+        if (left <= 0 || token >= p.tokens) continue;
+        int4v one = {0, 0, 0, 0}, two = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < S; ++w) {
+            one += *(const int4v *)(lds + w * C::kLds + t * ROW + ((c ^ (t & 7)) << 4));
+            if constexpr (C::GATED) two += *(const int4v *)(lds + w * C::kLds + t * ROW + (((c + LANES) ^ (t & 7)) << 4));
+        }
+        const float xs = p.x_scale ? p.x_scale[token] : 1.0f;
+        float y[4], u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t m = n + min((int64_t)e, left - 1);
+            y[e] = (float)one[e] * p.w_scale[m] * xs;
+            u[e] = C::GATED ? (float)two[e] * p.up_scale[m] * xs : 0.0f;
+            if (!C::GATED && p.bias) y[e] = y[e] + p.bias[m];
+        }
+        if constexpr (C::GATED)
+            with_activation(p.act, [&](auto act) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = act_value(decltype(act)::value, y[e]) * u[e];
+            });
+        store4(p.out, type, token * p.out_stride + n, left, whole, y);
+    }
+}
+
 template <bool GATED, int SHAPE = 0>
 void launch_tile(int shape, dim3 grid, dim3 block, const I8Product &p, int type, hipStream_t stream) {
-    if constexpr (SHAPE < kI8TileCount) {
+    if constexpr (SHAPE < kI8TileCount + kI8SplitCount) {
         if (shape != SHAPE) return launch_tile<GATED, SHAPE + 1>(shape, grid, block, p, type, stream);
-        hipLaunchKernelGGL((i8_tile_kernel<TileConfig<GATED, SHAPE>>), grid, block, 0, stream, p, type);
+        typedef TileConfig<GATED, SHAPE> C;
+        if constexpr (SHAPE < kI8TileCount) hipLaunchKernelGGL((i8_tile_kernel<C>), grid, block, 0, stream, p, type);
+        else hipLaunchKernelGGL((i8_split_kernel<C>), grid, block, 0, stream, p, type);
     }
 }
 
@@ -196,7 +257,7 @@ template <bool GATED>
 hipError_t run(const loom_launch_config &cfg, const I8Product &p, int type, hipStream_t stream) {
     const dim3 grid(cfg.workgroups[0]), block(cfg.workgroup_size[0]);
     if (p.tokens > i8_stream_max_tokens(GATED)) {
-        launch_tile<GATED>(i8_tile_choice(p.rows, 4 * (int64_t)p.kw, p.tokens, GATED), grid, block, p, type, stream);
+        launch_tile<GATED>(i8_tile_choice(p.rows, 4 * (int64_t)p.kw, p.tokens, GATED, true), grid, block, p, type, stream);
         return hipGetLastError();
     }
     switch (i8_stream_groups(p.tokens)) {

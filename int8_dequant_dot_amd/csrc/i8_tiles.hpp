@@ -129,10 +129,10 @@ struct TileConfig {
     static constexpr int NW = WM * WN, CH = WM * WT * 16, TK = WN * XT * 16;
     static constexpr int OUT_CH = GATED ? CH / 2 : CH;  // channels of the output
     static constexpr int kBytesW = CH * 128, kBytesX = TK * 128;  // one step
-    static constexpr int kStartX = kRingW * kBytesW, kLds = kStartX + kRingX * kBytesX;
+    static constexpr int kStartX = kRingW * kBytesW, kLds = kStartX + kRingX * kBytesX;  // of one tile
     static constexpr int WJ = CH / 8 / NW, XJ = TK / 8 / NW;  // direct loads a wave and step
     static_assert(CH % (8 * NW) == 0 && TK % (8 * NW) == 0 && (!GATED || WT % 2 == 0), "whole loads a wave");
-    static_assert(kLds == kShape.lds() && kLds <= 160 * 1024, "the launch's LDS");
+    static_assert(kLds * kShape.split == kShape.lds() && kShape.lds() <= 160 * 1024, "the launch's LDS");
     static_assert(kRingX >= 2 && kRingW >= kRingX && kRingW * WJ + kRingX * XJ <= 63, "the loads in flight can be counted");
 };
 
@@ -150,9 +150,13 @@ struct TileLoop {
 
     __device__ TileLoop(const I8Product &p_, char *lds_, int64_t n0_, int64_t t0_)
         : p(p_), lds(lds_), n0(n0_), t0(t0_), lane(lane_id()),
-          wave(__builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave))) {
+          wave(C::NW > 1 ? __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave)) : 0) {
         wm = wave % C::WM;
         wn = wave / C::WM;
+    }
+    // Waves of one tile meet; a wave with a tile of its own goes on.
+    __device__ __forceinline__ static void meet() {
+        if constexpr (C::NW > 1) barrier();
     }
 
     // LDS weight row r -> row of its matrix, relative to n0 (gated: the first
@@ -177,10 +181,11 @@ struct TileLoop {
         }
     }
 
-    // first: the step that comes first (the others follow it, round the end)
-    __device__ __forceinline__ void run(int4v (&acc)[C::WT][C::XT], int first) {
+    // Adds the products of `steps` whole steps from step `begin`, in the order
+    // first, first + 1, .. round the end, and where `tail` those of the partly
+    // filled step behind the last whole one.
+    __device__ __forceinline__ void run(int4v (&acc)[C::WT][C::XT], int begin, int steps, int first, bool tail) {
         const int64_t kb = 4 * (int64_t)p.kw;
-        const int steps = p.kw / 32;
         const int4v rw = buffer_over(p.w + n0 * p.kw, (p.rows - n0) * kb);
         const int4v ru = C::GATED ? buffer_over(p.w_up + n0 * p.kw, (p.rows - n0) * kb) : rw;
         const int4v rx = buffer_over(p.x + t0 * p.kw, (p.tokens - t0) * kb);
@@ -202,7 +207,7 @@ struct TileLoop {
         // Load j of the activations of step s, or of its weights, into that place.
         // A step past the end reads nothing: its buffers have size 0, so the loop
         // needs no branch for it.
-        auto at_step = [&](int s) { return s + first >= steps ? s + first - steps : s + first; };
+        auto at_step = [&](int s) { return begin + (s + first >= steps ? s + first - steps : s + first); };
         auto load_x = [&](int s, int place, int j) {
             int4v r = rx;
             r.z = s < steps ? r.z : 0;
@@ -224,12 +229,12 @@ struct TileLoop {
         // Two rounds through one copy of the loop (two copies cost the
         // accumulators their registers): first the rest of k, a partly filled
         // step staged word by word, then the whole steps.
-        int round = p.kw % 32 ? 0 : 1;
+        int round = tail ? 0 : 1;
         if (steps == 0 && round == 1) return;
         do {
             const int count = round == 0 ? 1 : steps;
             if (round == 0) {
-                for (int c = threadIdx.x; c < (C::CH + C::TK) * 8; c += C::NW * kWave) {
+                for (int c = C::NW > 1 ? (int)threadIdx.x : lane; c < (C::CH + C::TK) * 8; c += C::NW * kWave) {
                     const int r = c >> 3, q = c & 7;
                     const int32_t *row;
                     if (r < C::CH) row = (is_up(r) ? p.w_up : p.w) + (n0 + min(weight_row(r), left_n - 1)) * p.kw;
@@ -237,16 +242,16 @@ struct TileLoop {
                     int4v v = {0, 0, 0, 0};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int at_word = steps * 32 + q * 4 + e;
+                        const int at_word = p.kw / 32 * 32 + q * 4 + e;
                         if (at_word < p.kw) v[e] = row[at_word];
                     }
                     *(int4v *)(lds + (r < C::CH ? r * 128 : C::kStartX + (r - C::CH) * 128) + ((q ^ (r & 7)) << 4)) = v;
                 }
                 wait_lds();
             } else {
-                barrier();  // every wave has read what the first round left
+                meet();  // every wave has read what the first round left
                 // in the order in which the steps before the first would load them
-#pragma unroll
+#pragma unroll 1
                 for (int s = 0; s < C::kRingW; ++s) {
                     const int sx = s + C::kRingX - C::kRingW;
                     if (sx >= 0)
@@ -258,7 +263,7 @@ struct TileLoop {
                 // what came after x(0), and w(0) where that was later
                 wait_loads<(C::kRingX - 1) * J + (C::kRingW > C::kRingX ? C::WJ : 0)>();
             }
-            barrier();
+            meet();
             TileFragments<C> f0, f1;
             each_index<kReads>([&](auto r) { read<decltype(r)::value>(f0, 0, C::kStartX, 0); });
             const int skip = round == 0 ? steps : 0;  // the first round loads nothing
@@ -275,7 +280,7 @@ struct TileLoop {
                     });
                     if constexpr (q == L) {
                         wait_lds();
-                        barrier();
+                        meet();
                     }
                     each_index<J>([&](auto at_j) {
                         constexpr int j = decltype(at_j)::value;
@@ -294,7 +299,7 @@ struct TileLoop {
                 here_x = here_x == C::kLds - C::kBytesX ? C::kStartX : here_x + C::kBytesX;
                 // what came after x(s + 1), and w(s + 1) where that was later
                 wait_loads<(C::kRingX - 2) * J + EARLY + (C::kRingW > C::kRingX ? C::WJ : 0)>();
-                barrier();
+                meet();
                 each_index<Q>([&](auto at_q) {
                     constexpr int q = decltype(at_q)::value;
                     each_index<kReads>([&](auto at_r) {

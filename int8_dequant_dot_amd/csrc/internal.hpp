@@ -430,15 +430,18 @@ struct I8TileShape {
     int ring_w, ring_x;          // steps of 128 bytes of k in LDS
     int resident;                // workgroups of a CU
     double step_us;              // one step of a workgroup that has its CU to itself
+    int split = 1;               // waves that share k, each with the tile and rings of its own
     constexpr int channels() const { return wm * wt * 16; }
     constexpr int tokens() const { return wn * xt * 16; }
-    constexpr int waves() const { return wm * wn; }
-    constexpr int lds() const { return (ring_w * channels() + ring_x * tokens()) * 128; }
+    constexpr int waves() const { return wm * wn * split; }
+    constexpr int lds() const { return split * (ring_w * channels() + ring_x * tokens()) * 128; }
 };
 constexpr I8TileShape kI8Tiles[] = {
     {1, 2, 2, 1, 5, 5, 4, 0.21}, {2, 2, 2, 1, 6, 6, 2, 0.27}, {2, 2, 2, 2, 5, 5, 2, 0.29}, {2, 2, 4, 2, 3, 3, 2, 0.40},
-    {2, 2, 2, 4, 3, 3, 2, 0.36}, {2, 2, 4, 4, 5, 5, 1, 0.54}, {2, 2, 4, 8, 4, 3, 1, 0.85}, {2, 2, 8, 8, 2, 2, 1, 1.27}};
-constexpr int kI8TileCount = 8;
+    {2, 2, 2, 4, 3, 3, 2, 0.36}, {2, 2, 4, 4, 5, 5, 1, 0.54}, {2, 2, 4, 8, 4, 3, 1, 0.85}, {2, 2, 8, 8, 2, 2, 1, 1.27},
+    {1, 1, 2, 2, 4, 4, 1, 0.30, 4}, {1, 1, 2, 4, 3, 3, 1, 0.43, 4}};
+constexpr int kI8TileCount = 8;   // shapes whose waves share the tile
+constexpr int kI8SplitCount = 2;  // and shapes that split k, for the product and the gated projection
 constexpr int kI8StreamWaves = 4;  // 1, 2 and 8 waves were up to 30, 8 and 20 % slower, rarely faster
 constexpr int kI8StreamRows = 16;
 constexpr int i8_stream_max_tokens(bool gated) { return gated ? 8 : 16; }
@@ -455,12 +458,15 @@ constexpr int64_t i8_tile_count(const I8TileShape &t, int64_t rows, int64_t toke
 // reach from its L2) and their products at 16.4 M operations/us; the launch takes
 // its rounds, or the memory's time for the weights at 6 TB/s if that is longer.
 // Over 156 sizes (500 to 28672 channels, 17 to 2048 tokens, k 1024 to 28672) the
-// shape so chosen took 1 % longer on average than the fastest of the eight, at
+// shape so chosen took 1 % longer on average than the fastest of the first eight, at
 // worst 14 %; the 256 x 256 shape alone took 3 times as long on average.
-constexpr int i8_tile_choice(int64_t rows, int64_t k, int64_t tokens, bool gated) {
+// The shapes that split k serve launches of one round: 17 to 32 tokens x 500
+// channels x k 16000 22 -> 11 us, 21 x 4099 x 11008 16.6 -> 12.2 us; two rounds of
+// them lose (gated 17 x 4099 x 11008 19 -> 23 us), as the estimate says.
+constexpr int i8_tile_choice(int64_t rows, int64_t k, int64_t tokens, bool gated, bool split) {
     int best = 0;
     double best_us = 0;
-    for (int i = 0; i < kI8TileCount; ++i) {
+    for (int i = 0; i < kI8TileCount + (split ? kI8SplitCount : 0); ++i) {
         const I8TileShape &t = kI8Tiles[i];
         const int64_t tiles = i8_tile_count(t, rows, tokens, gated), round = 256 * t.resident;
         const int64_t full = tiles / round, rest = ceil_of(tiles % round, 256);
@@ -468,11 +474,11 @@ constexpr int i8_tile_choice(int64_t rows, int64_t k, int64_t tokens, bool gated
         for (int last = 0; last < 2; ++last) {
             const double r = last ? (double)rest : (double)t.resident, times = last ? (rest > 0) : (double)full;
             double step = t.step_us;
-            const double load = r * (t.channels() + t.tokens()) * 128 / 58e3;
-            const double math = r * t.channels() * t.tokens() * 256.0 / 16.4e6;
+            const double load = r * t.split * (t.channels() + t.tokens()) * 128 / 58e3;
+            const double math = r * t.split * t.channels() * t.tokens() * 256.0 / 16.4e6;
             if (load > step) step = load;
             if (math > step) step = math;
-            us += times * (step * (double)k / 128 + 1);
+            us += times * (step * (double)k / (128 * t.split) + (t.split > 1 ? 3 : 1));
         }
         const double memory = ((double)rows * (gated ? 2 : 1) + (double)tokens) * (double)k / 6e6;
         if (memory > us) us = memory;
@@ -578,7 +584,7 @@ constexpr I8BackwardSpace i8_backward_space(int64_t rows, int64_t k, int64_t tok
     const int64_t coef = 4 * i8_limbs(type) * tokens * padded;
     const I8DxPlan plan = i8_dx_plan(rows, k, tokens, type);
     const int64_t dx = plan.splits > 1 ? 4 * plan.splits * tokens * k : 0;
-    const int64_t tiles = ceil_of(tokens, kI8Tiles[i8_tile_choice(rows, k, tokens, true)].tokens());
+    const int64_t tiles = ceil_of(tokens, kI8Tiles[i8_tile_choice(rows, k, tokens, true, false)].tokens());
     const int64_t parts = ceil_of(coef, 256) * 256, sums = parts + ceil_of(dx, 256) * 256;
     return I8BackwardSpace{parts, sums, sums + 8 * rows * tiles};
 }

@@ -164,14 +164,14 @@ int geo_quantize_rows(const int64_t *w, loom_launch_config *c) {
 // i8_matmul, i8_gated_projection (rows, k, tokens): few tokens take one
 // workgroup per kI8StreamRows weight rows (LDS: its waves' partial sums); more
 // take one per tile of i8_tile_choice.
-int geo_i8_tiles(const int64_t *w, bool gated, loom_launch_config *c) {
-    const I8TileShape &t = kI8Tiles[i8_tile_choice(w[0], w[1], w[2], gated)];
+int geo_i8_tiles(const int64_t *w, bool gated, bool split, loom_launch_config *c) {
+    const I8TileShape &t = kI8Tiles[i8_tile_choice(w[0], w[1], w[2], gated, split)];
     return set(c, i8_tile_count(t, w[0], w[2], gated), (uint32_t)(t.waves() * kSubgroupSize), (uint32_t)t.lds());
 }
 template <bool GATED>
 int geo_i8_product(const int64_t *w, loom_launch_config *c) {
     if (w[0] < 0 || w[1] < 0 || w[2] < 0) return LOOM_ERR_RANGE;
-    if (w[2] > i8_stream_max_tokens(GATED)) return geo_i8_tiles(w, GATED, c);
+    if (w[2] > i8_stream_max_tokens(GATED)) return geo_i8_tiles(w, GATED, true, c);
     const int64_t groups = w[2] > 0 ? ceil_div(w[0], kI8StreamRows / (GATED ? 2 : 1)) : 0;
     return set(c, groups, kI8StreamWaves * kSubgroupSize,
                (uint32_t)(kI8StreamWaves * kI8StreamRows * 16 * i8_stream_groups(w[2])));
@@ -183,7 +183,7 @@ int geo_i8_backward(const int64_t *w, loom_launch_config *c) {
     if (w[0] < 0 || w[1] < 0 || w[2] < 0 || w[0] > kI8BackwardMaxRows) return LOOM_ERR_RANGE;
     // the second kernel's grid, of at least 32 tokens x 128 columns x 256 work-items a tile
     if (ceil_div(w[2], 32) > kMaxGridWorkItems / 256 / (ceil_div(w[1], 128) + 1)) return LOOM_ERR_RANGE;
-    return geo_i8_tiles(w, true, c);
+    return geo_i8_tiles(w, true, false, c);
 }
 
 struct Export {
