@@ -55,7 +55,7 @@ __global__ __launch_bounds__(C::NW * kWave, 1) void coefficients_kernel(I8Produc
     typedef TileOut<C, true> Out;
     __shared__ __align__(1024) char lds[C::kLds];
     uint32_t ch, tok;
-    tile_of(blockIdx.x, (p.rows + C::OUT_CH - 1) / C::OUT_CH, (p.tokens + C::TK - 1) / C::TK, 8, ch, tok);
+    tile_of(blockIdx.x, count_of(p.rows, C::OUT_CH), count_of(p.tokens, C::TK), 8, ch, tok);
     TileLoop<C> loop(p, lds, (int64_t)ch * C::OUT_CH, (int64_t)tok * C::TK);
     int4v acc[C::WT][C::XT];
 #pragma unroll
@@ -399,7 +399,7 @@ template <typename C>
 __global__ __launch_bounds__(C::NW * kWave, 1) void d_x_kernel(I8Product p, DxOperands o) {
     __shared__ __align__(1024) char lds[C::kLds];
     uint32_t ch, tok;
-    tile_of(blockIdx.x, (uint32_t)((o.k + C::TI - 1) / C::TI), (p.tokens + C::TK - 1) / C::TK, 8, ch, tok);
+    tile_of(blockIdx.x, count_of((int)o.k, C::TI), count_of(p.tokens, C::TK), 8, ch, tok);
     DxLoop<C> loop(p, o, lds, (int64_t)ch * C::TI, (int64_t)tok * C::TK);
     int4v acc[C::WT][C::XT];
 #pragma unroll

@@ -137,7 +137,7 @@ template <typename C>
 __global__ __launch_bounds__(C::NW * kWave, 1) void i8_tile_kernel(I8Product p, int type) {
     __shared__ __align__(1024) char lds[C::kLds];
     uint32_t ch, tok;
-    tile_of(blockIdx.x, (p.rows + C::OUT_CH - 1) / C::OUT_CH, (p.tokens + C::TK - 1) / C::TK, 8, ch, tok);
+    tile_of(blockIdx.x, count_of(p.rows, C::OUT_CH), count_of(p.tokens, C::TK), 8, ch, tok);
     TileLoop<C> loop(p, lds, (int64_t)ch * C::OUT_CH, (int64_t)tok * C::TK);
     int4v acc[C::WT][C::XT];
 #pragma unroll
@@ -196,7 +196,7 @@ __global__ __launch_bounds__(C::kShape.waves() * kWave, 1) void i8_split_kernel(
     static_assert(C::CH == 32 && C::kLds >= C::TK * ROW, "the sums fit the rings");
     __shared__ __align__(1024) char lds[S * C::kLds];
     uint32_t ch, tok;
-    tile_of(blockIdx.x, (p.rows + C::OUT_CH - 1) / C::OUT_CH, (p.tokens + C::TK - 1) / C::TK, 8, ch, tok);
+    tile_of(blockIdx.x, count_of(p.rows, C::OUT_CH), count_of(p.tokens, C::TK), 8, ch, tok);
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave)), lane = lane_id();
     TileLoop<C> loop(p, lds + wave * C::kLds, (int64_t)ch * C::OUT_CH, (int64_t)tok * C::TK);
     int4v acc[C::WT][C::XT];

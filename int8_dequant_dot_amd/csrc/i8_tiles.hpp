@@ -87,6 +87,7 @@ __device__ __forceinline__ void settle(int4v (&acc)[N][M]) {
 // contiguous run of a tile order in which `high` token tiles alternate fastest:
 // its 32 CUs then work on a compact rectangle of the output and share its
 // weight and activation rows.
+__device__ __forceinline__ uint32_t count_of(int n, int tile) { return ((uint32_t)n + tile - 1) / tile; }
 __device__ __forceinline__ void tile_of(uint32_t block, uint32_t ch_tiles, uint32_t tok_tiles, uint32_t high,
                                         uint32_t &ch, uint32_t &tok) {
     const uint32_t total = ch_tiles * tok_tiles, q = total / 8, r = total % 8;
