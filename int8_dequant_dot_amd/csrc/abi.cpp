@@ -332,8 +332,10 @@ extern "C" int loom_i8_gated_projection_backward(const int32_t *w_gate, const fl
         return LOOM_ERR_ALIGN;
     const loom::I8Product p = {w_gate,    gate_scale,  w_up,         up_scale, x,       x_scale, nullptr,
                                (int)rows, (int)tokens, (int)(k / 4), act,      nullptr, 0};
+    const auto run = type == LOOM_F32   ? loom::launch_i8_gated_backward_f32
+                     : type == LOOM_F16 ? loom::launch_i8_gated_backward_f16
+                                        : loom::launch_i8_gated_backward_bf16;
     return launch([&] {
-        return loom::launch_i8_gated_projection_backward(cfg, p, d_out, type, d_stride, d_x, d_gate_scale, d_up_scale,
-                                                         workspace, (hipStream_t)stream);
+        return run(cfg, p, d_out, d_stride, d_x, d_gate_scale, d_up_scale, workspace, (hipStream_t)stream);
     });
 }

@@ -1,4 +1,4 @@
-// i8_gated_backward.hip -- gradients of the gated projection.
+// i8_gated_backward.hpp -- gradients of the gated projection.
 //
 // With g, u the two scaled products (recomputed: the int32 sums are exact, so
 // they are the forward pass's bits) and d the gradient of the output,
@@ -13,6 +13,8 @@
 // bfloat16, so only the coefficients are rounded, once to 8 bits for bfloat16
 // gradients (as d_out itself was, and as the result will be), to 16 bits or more
 // for float16 ones and not at all for float32 ones.  All sums are f32.
+#pragma once
+
 #include <algorithm>
 
 #include "i8_tiles.hpp"
@@ -470,7 +472,7 @@ void launch_d_x(const I8DxPlan &plan, const I8Product &p, const DxOperands &o, h
 }
 
 template <int LIMBS>
-hipError_t run(const loom_launch_config &cfg, const I8Product &p, const void *d_out, int type, int64_t d_stride,
+hipError_t run_backward(const loom_launch_config &cfg, const I8Product &p, const void *d_out, int type, int64_t d_stride,
                void *d_x, float *d_gate, float *d_up, void *workspace, hipStream_t stream) {
     const int64_t rows = p.rows, tokens = p.tokens, k = 4 * (int64_t)p.kw;
     const I8BackwardSpace space = i8_backward_space(rows, k, tokens, type);
@@ -516,13 +518,5 @@ hipError_t run(const loom_launch_config &cfg, const I8Product &p, const void *d_
 }
 
 }  // namespace
-
-hipError_t launch_i8_gated_projection_backward(const loom_launch_config &cfg, const I8Product &p, const void *d_out,
-                                               int type, int64_t d_stride, void *d_x, float *d_gate, float *d_up,
-                                               void *workspace, hipStream_t stream) {
-    if (type == LOOM_F32) return run<3>(cfg, p, d_out, type, d_stride, d_x, d_gate, d_up, workspace, stream);
-    if (type == LOOM_F16) return run<2>(cfg, p, d_out, type, d_stride, d_x, d_gate, d_up, workspace, stream);
-    return run<1>(cfg, p, d_out, type, d_stride, d_x, d_gate, d_up, workspace, stream);
-}
 
 }  // namespace loom

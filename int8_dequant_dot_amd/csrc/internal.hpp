@@ -632,10 +632,16 @@ hipError_t launch_i8_matmul(const loom_launch_config &cfg, const I8Product &p, i
 hipError_t launch_i8_gated_projection(const loom_launch_config &cfg, const I8Product &p, int type,
                                       hipStream_t stream);
 
-// type, d_stride: of d_out; d_x (same type), d_gate and d_up may each be NULL
+// One function a type of d_out and d_x; d_stride: of d_out; d_x, d_gate and d_up may each be NULL
 // (not wanted).
-hipError_t launch_i8_gated_projection_backward(const loom_launch_config &cfg, const I8Product &p, const void *d_out,
-                                               int type, int64_t d_stride, void *d_x, float *d_gate, float *d_up,
-                                               void *workspace, hipStream_t stream);
+hipError_t launch_i8_gated_backward_f32(const loom_launch_config &cfg, const I8Product &p, const void *d_out,
+                                        int64_t d_stride, void *d_x, float *d_gate, float *d_up, void *workspace,
+                                        hipStream_t stream);
+hipError_t launch_i8_gated_backward_f16(const loom_launch_config &cfg, const I8Product &p, const void *d_out,
+                                        int64_t d_stride, void *d_x, float *d_gate, float *d_up, void *workspace,
+                                        hipStream_t stream);
+hipError_t launch_i8_gated_backward_bf16(const loom_launch_config &cfg, const I8Product &p, const void *d_out,
+                                         int64_t d_stride, void *d_x, float *d_gate, float *d_up, void *workspace,
+                                         hipStream_t stream);
 
 }  // namespace loom
