@@ -398,7 +398,11 @@ int loom_i8_gated_projection(const int32_t *w_gate, const float *gate_scale, con
  *     d_up_scale[f]   = sum_t du[t][f] acc_up[t][f] x_scale[t]              *
  * d_x is the gradient of the dequantised activation x * x_scale, what a     *
  * straight-through estimator passes on.  ReLU's derivative at 0 is 0.  All  *
- * sums are f32 in a fixed order: the same bits on every call.               *
+ * sums are f32 in a fixed order: the same bits on every call.  d_x is a     *
+ * product of the weights and the coefficients dg gate_scale, du up_scale,   *
+ * which are whole for f32 gradients, rounded to at least 16 bits for f16    *
+ * ones and to 11 bits for bf16 ones (there by at most 2^-30 of the token's  *
+ * largest coefficient where that is more), and d_x is then rounded once.    *
  *   d_out        : type[tokens], rows d_stride >= rows elements apart       *
  *   d_x          : type[tokens][k] (the type of d_out), device, or NULL     *
  *   d_gate_scale, d_up_scale : f32[rows], device, or NULL                   *

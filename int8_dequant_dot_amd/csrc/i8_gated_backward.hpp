@@ -8,11 +8,17 @@
 //     d_up_scale[f]     = sum_t du[t][f] acc_up[t][f] x_scale[t]
 // d_x is the gradient with respect to the dequantised activation x * x_scale.
 //
-// The coefficients dg gate_scale and du up_scale go to memory as bfloat16 limbs,
-// and d_x is a bfloat16 product on the matrix cores: the int8 weights are exact in
-// bfloat16, so only the coefficients are rounded, once to 8 bits for bfloat16
-// gradients (as d_out itself was, and as the result will be), to 16 bits or more
-// for float16 ones and not at all for float32 ones.  All sums are f32.
+// The coefficients dg gate_scale and du up_scale go to memory as 16-bit limbs, and
+// d_x is a product of them on the matrix cores: the int8 weights are exact in
+// bfloat16 and in float16, so only the coefficients are rounded.  For float16
+// gradients they are two bfloat16 limbs (16 bits or more), for float32 ones three
+// (exact).  For bfloat16 gradients, which have 8 bits themselves, they are one
+// float16 limb: 11 bits, an eighth of what the last rounding of d_x loses, at the
+// cost of one limb.  Its exponents have the range of one power of two for each
+// token: float16 is full down to 2^-20 of the token's largest coefficient, and
+// what is below is off by at most 2^-30 of that coefficient.  All sums are f32.
+// (One bfloat16 limb was as fast, and its rounding as large as d_x's own: 0.0023 of
+// d_x against 0.0017.  Two would double d_x's products.)
 #pragma once
 
 #include <algorithm>
@@ -38,16 +44,39 @@ __device__ __forceinline__ void limbs_of(float c, uint32_t (&limb)[LIMBS]) {
     limb[LIMBS - 1] = bf16_bits(c);
 }
 
+// The power of two that a block of float16 coefficients is divided by: 2^(8 e) with
+// the block's largest magnitude, `top`, in 2^6 .. 2^14 of it, so that blocks that
+// are as large as each other mostly have the same.  Infinite ones get the largest.
+__device__ __forceinline__ int block_exponent(float top) {
+    const int e = ((int)(__builtin_bit_cast(uint32_t, top) >> 23) - 133) >> 3;
+    return e < -15 ? -15 : e;
+}
+__device__ __forceinline__ float power_of_two(int e) { return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ uint32_t f16_bits(float c) { return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)c); }
+
 struct Coefficients {
     const void *d_out;
     int64_t d_stride;
     int type;
     uint16_t *coef;  // [limbs][tokens][2][padded], or NULL
     int64_t padded;
+    int8_t *exponents;  // [tokens][blocks of a wave's channels], one limb only
+    int64_t blocks;
     float *sums;     // [token tiles][2][rows]
     float *scale[2]; // one token tile: the scale gradients themselves, or NULL
     bool whole_sums; // there is one token tile
 };
+
+// The largest of non-negative numbers over each aligned group of 4, 8 or 16 lanes.
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {
+    v = fmaxf(v, dpp<kDppQuadSwap1>(v));
+    v = fmaxf(v, dpp<kDppQuadSwap2>(v));
+    if constexpr (LANES >= 8) v = fmaxf(v, dpp<kDppHalfMirror>(v));
+    if constexpr (LANES >= 16) v = fmaxf(v, dpp<kDppMirror>(v));
+    static_assert(LANES == 4 || LANES == 8 || LANES == 16, "the steps above");
+    return v;
+}
 
 // Both products again, then d_x's coefficients and the tile's terms of the scale
 // gradients: a lane adds the terms of its four channels over its tokens, then the
@@ -130,12 +159,30 @@ __global__ __launch_bounds__(C::NW * kWave, 1) void coefficients_kernel(I8Produc
 #pragma unroll
         for (int j = 0; j < Out::GROUP; ++j) {
             uint32_t lg[4][LIMBS], lu[4][LIMBS];
+            int exponent = 0;
+            if constexpr (LIMBS == 1) {
+                // a block: the wave's channels of the token, in Out::LANES neighbouring lanes
+                float top = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < left) top = fmaxf(top, fmaxf(fabsf(cg[j][e]), fabsf(cu[j][e])));
+                exponent = block_exponent(lanes_max<Out::LANES>(top));
+            }
+            const float scale = power_of_two(-8 * exponent);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                limbs_of<LIMBS>(e < left ? cg[j][e] : 0.0f, lg[e]);
-                limbs_of<LIMBS>(e < left ? cu[j][e] : 0.0f, lu[e]);
+                const float g = e < left ? cg[j][e] : 0.0f, u = e < left ? cu[j][e] : 0.0f;
+                if constexpr (LIMBS == 1) {
+                    lg[e][0] = f16_bits(g * scale);
+                    lu[e][0] = f16_bits(u * scale);
+                } else {
+                    limbs_of<LIMBS>(g, lg[e]);
+                    limbs_of<LIMBS>(u, lu[e]);
+                }
             }
             if (!pass[j].live) continue;
+            if (LIMBS == 1 && loop.lane % Out::LANES == 0 && n < p.rows)
+                o.exponents[(t1 + (pass[0].i + j) * Out::PER) * o.blocks + n / Out::OC] = (int8_t)exponent;
 #pragma unroll
             for (int i = 0; i < LIMBS; ++i) {
                 uint16_t *row = o.coef + start + (pass[0].i + j) * by + i * limb;
@@ -194,15 +241,71 @@ __global__ __launch_bounds__(256) void scale_gradients_kernel(const float *__res
     if (to) to[c < rows ? c : c - rows] = sum;
 }
 
+// One power of two a token for its float16 coefficients: the largest of its blocks'.
+// Blocks that were divided by another are divided again, in place (a few in ten where
+// the coefficients are alike, as their powers are 2^8 apart); a workgroup a token.
+// 1003 tokens x 11008 channels: 7 us; 2048 x 28672: 41 us (one place of four channels
+// at a time 10 and 54 us).
+__global__ __launch_bounds__(256) void token_powers_kernel(uint16_t *coef, int64_t padded, int64_t tokens, int rows,
+                                                           const int8_t *__restrict__ exponents, int block,
+                                                           float *__restrict__ powers) {
+    __shared__ int tops[4];
+    const int blocks = (rows + block - 1) / block, shift = __builtin_ctz(block);  // block: a power of two
+    for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+        const int8_t *mine = exponents + t * blocks;
+        int top = -15;
+        for (int b = threadIdx.x; b < blocks; b += 256) top = max(top, (int)mine[b]);
+#pragma unroll
+        for (int far = 1; far < kWave; far *= 2) top = max(top, __shfl_xor(top, far));
+        if (lane_id() == 0) tops[threadIdx.x / kWave] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, tops[i]);
+        __syncthreads();
+        if (threadIdx.x == 0) powers[t] = power_of_two(8 * top);
+        // PLACES places of four channels at once, their reads in flight together
+        constexpr int PLACES = 8;
+        typedef _Float16 Half4 __attribute__((ext_vector_type(4)));
+        for (int first = 4 * threadIdx.x; first < rows; first += 4 * 256 * PLACES) {
+            int by[PLACES];
+            Half4 c[PLACES][2];
+#pragma unroll
+            for (int i = 0; i < PLACES; ++i) {
+                const int n = first + i * 4 * 256;
+                by[i] = n < rows ? top - mine[n >> shift] : 0;
+            }
+            Half4 *at = (Half4 *)(coef + 2 * t * padded + first), *up = (Half4 *)((uint16_t *)at + padded);
+#pragma unroll
+            for (int i = 0; i < PLACES; ++i)
+                if (by[i]) {
+                    c[i][0] = at[i * 256];
+                    c[i][1] = up[i * 256];
+                }
+#pragma unroll
+            for (int i = 0; i < PLACES; ++i)
+                if (by[i]) {
+                    const float scale = power_of_two(by[i] > 15 ? -120 : -8 * by[i]);
+                    auto divided = [&](Half4 h) {
+                        return Half4{(_Float16)((float)h[0] * scale), (_Float16)((float)h[1] * scale),
+                                     (_Float16)((float)h[2] * scale), (_Float16)((float)h[3] * scale)};
+                    };
+                    at[i * 256] = divided(c[i][0]);
+                    up[i * 256] = divided(c[i][1]);
+                }
+        }
+    }
+}
+
 // ---------------------------------------------------------------- d_x
 // D[i][t] = sum_f w[f][i] c[t][f] over the gate rows f, then the up rows, in steps
 // of 64 rows.  LDS holds a ring of steps: 64 rows x TI bytes of weights and, for
-// each limb, TK tokens x 64 bfloat16 coefficients, 16-byte chunk c of row r at
+// each limb, TK tokens x 64 coefficients, 16-byte chunk c of row r at
 // slot c ^ (r % chunks) in both.  The A operand (16 columns i, 8 neighbouring f a
 // lane) is the weights' transpose: ds_read_b64_tr_b8 hands each lane of a group of
-// 16 one column of 8 rows x 16 bytes.  Those 8 bytes become bfloat16 while the
-// products of the fragment before run: 8 conversions and 4 byte permutes for
-// XT * LIMBS products.
+// 16 one column of 8 rows x 16 bytes.  Those 8 bytes become bfloat16, or float16 for
+// one limb, while the products of the fragment before run: 8 conversions and 4 byte
+// permutes, or 2 exclusive ors, 4 byte permutes and 4 subtractions, for XT * LIMBS
+// products.
 // 2048 tokens x 28672 channels x k 8192 in tiles of 256 x 256: 1.40 to 1.45 ms (1.3
 // to 1.4 PFLOP/s), the matrix cores 64 % busy at the clock their power leaves; with
 // waves of 128 x 128, which convert every weight fragment twice, 1.55 ms; without
@@ -231,9 +334,11 @@ struct DxOperands {
 };
 
 // FRESH: a was converted just before (two wait states from a vector instruction).
-template <bool FRESH>
-__device__ __forceinline__ void mfma_bf16(int4v &acc, int4v a, int4v b) {
-    if constexpr (FRESH) asm("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+template <bool HALF, bool FRESH>
+__device__ __forceinline__ void mfma_16(int4v &acc, int4v a, int4v b) {
+    if constexpr (HALF && FRESH) asm("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+    else if constexpr (HALF) asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+    else if constexpr (FRESH) asm("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
     else asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
 
@@ -280,10 +385,16 @@ struct DxLoop {
     }
 
     // Elements 2 J, 2 J + 1 of a fragment as bfloat16: an int8's f32 has no bits
-    // below the upper half.
+    // below the upper half.  As float16: 0x6400 + b is 1024 + b, and b the element
+    // plus 128.
     template <int J>
     __device__ static __forceinline__ uint32_t pair(uint2v raw) {
         const uint32_t w = raw[J / 2];
+        if constexpr (C::LIMBS == 1) {
+            typedef _Float16 Half2 __attribute__((ext_vector_type(2)));
+            const uint32_t b = __builtin_amdgcn_perm(0x64646464u, w ^ 0x80808080u, J % 2 ? 0x04030402u : 0x04010400u);
+            return __builtin_bit_cast(uint32_t, __builtin_bit_cast(Half2, b) - Half2{(_Float16)1152, (_Float16)1152});
+        }
         const float lo = (float)(int8_t)(w >> (16 * (J % 2))), hi = (float)(int8_t)(w >> (16 * (J % 2) + 8));
         return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
     }
@@ -351,7 +462,7 @@ struct DxLoop {
                     ready[(i + 1) % 2][j] = pair<j>(i + 1 < C::WT ? f.a[i + 1 < C::WT ? i + 1 : 0] : g.a[0]);
             });
             const int4v a = {(int)ready[i % 2][0], (int)ready[i % 2][1], (int)ready[i % 2][2], (int)ready[i % 2][3]};
-            mfma_bf16<in == 0>(acc[i][in % C::XT], a, f.b[in / C::XT][in % C::XT]);
+            mfma_16<C::LIMBS == 1, in == 0>(acc[i][in % C::XT], a, f.b[in / C::XT][in % C::XT]);
         };
         static_assert(C::WT % 2 == 0, "a half step ends on the pair it began on");
         int s = first, here = 0;
@@ -425,7 +536,10 @@ __global__ __launch_bounds__(C::NW * kWave, 1) void d_x_kernel(I8Product p, DxOp
         for (int j = 0; j < Out::GROUP; ++j) {
             live[j] = pass[j].live;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[j][e] = __builtin_bit_cast(float, (int)pass[j].one[e]);
+            for (int e = 0; e < 4; ++e) {
+                y[j][e] = __builtin_bit_cast(float, (int)pass[j].one[e]);
+                if (C::LIMBS == 1) y[j][e] = y[j][e] * pass[j].scale;  // the token's power of two
+            }
         }
         store4_each(out, type, start + pass[0].i * by, by, left, whole, live, y);
     });
@@ -482,8 +596,12 @@ hipError_t run_backward(const loom_launch_config &cfg, const I8Product &p, const
     uint16_t *coef = inputs ? (uint16_t *)workspace : nullptr;
     float *sums = scales ? (float *)((char *)workspace + space.sums) : nullptr;
     const bool one = tokens > 0 && tokens <= kI8Tiles[shape].tokens();
+    const int block = kI8Tiles[shape].wave_channels();
+    const int64_t blocks = ceil_of(rows, block);
+    int8_t *exponents = (int8_t *)workspace + space.exponents;
+    float *powers = (float *)((char *)workspace + space.powers);
     if (tokens > 0 && rows > 0) {
-        const Coefficients o = {d_out, d_stride, type, coef, padded, one ? nullptr : sums,
+        const Coefficients o = {d_out, d_stride, type, coef, padded, exponents, blocks, one ? nullptr : sums,
                                 {one ? d_gate : nullptr, one ? d_up : nullptr}, one};
         launch_coefficients<LIMBS>(shape, dim3(cfg.workgroups[0]), dim3(cfg.workgroup_size[0]), p, o, stream);
     }
@@ -500,8 +618,11 @@ hipError_t run_backward(const loom_launch_config &cfg, const I8Product &p, const
     }
     const I8DxPlan plan = i8_dx_plan(rows, k, tokens, type);
     float *parts = (float *)((char *)workspace + space.parts);
+    if (LIMBS == 1)
+        hipLaunchKernelGGL(token_powers_kernel, dim3((uint32_t)std::min<int64_t>(tokens, 1 << 20)), dim3(256), 0, stream,
+                           coef, padded, tokens, p.rows, exponents, block, powers);
     I8Product plain = p;
-    plain.x_scale = nullptr;  // the tile's output applies it
+    plain.x_scale = LIMBS == 1 ? powers : nullptr;  // the tile's output applies it
     const DxOperands o = {{(const int8_t *)p.w, (const int8_t *)p.w_up}, coef, padded, rows, k, plan.splits,
                           plan.splits > 1 ? (void *)parts : d_x, type};
     switch (plan.shape) {

@@ -434,6 +434,7 @@ struct I8TileShape {
     constexpr int channels() const { return wm * wt * 16; }
     constexpr int tokens() const { return wn * xt * 16; }
     constexpr int waves() const { return wm * wn * split; }
+    constexpr int wave_channels() const { return wt * 8; }  // output channels of a wave, gated
     constexpr int lds() const { return split * (ring_w * channels() + ring_x * tokens()) * 128; }
 };
 constexpr I8TileShape kI8Tiles[] = {
@@ -507,13 +508,15 @@ struct I8Product {
 };
 
 // The gradients of the gated projection.  The first kernel computes both
-// products again in tiles of i8_tile_choice and leaves the coefficients of d_x,
-// bfloat16 [limbs][tokens][2][channels, padded with zeros to 64] (a coefficient
-// is the sum of its limbs: 8 bits each, one for bfloat16 gradients, 2 for float16,
-// 3 for float32), and each token tile's terms of the scale gradients.  The second
+// products again in tiles of i8_tile_choice and leaves the coefficients of d_x
+// and each token tile's terms of the scale gradients.  The coefficients are
+// 16-bit limbs [limbs][tokens][2][channels, padded with zeros to 64], a coefficient
+// the sum of its limbs: bfloat16 ones of 8 bits each, two for float16 gradients
+// and three for float32 ones; one float16 limb of 11 bits for bfloat16 gradients,
+// whose exponents a second kernel brings to one power of two a token.  The next
 // multiplies the coefficients by the weights, in tiles of one of these shapes
 // (columns of d_x x tokens), its steps split over workgroups where the tiles are
-// few; a third adds the parts.
+// few; a last one adds the parts.
 constexpr int kI8ChannelPad = 64;
 constexpr int64_t kI8BackwardMaxRows = (int64_t)1 << 21;  // 32-bit offsets within a token tile's coefficients
 constexpr int i8_limbs(int type) { return type == LOOM_BF16 ? 1 : type == LOOM_F16 ? 2 : 3; }
@@ -577,16 +580,25 @@ constexpr I8DxPlan i8_dx_plan(int64_t rows, int64_t k, int64_t tokens, int type)
 
 // Where the parts of the gradients' workspace begin, and its size.
 struct I8BackwardSpace {
-    int64_t parts, sums, bytes;  // d_x parts, scale terms (bytes from the start); the coefficients come first
+    // bytes from the start, where the coefficients are: d_x parts, scale terms, and for one limb the exponents of
+    // blocks of coefficients and the tokens' powers of two
+    int64_t parts, sums, exponents, powers, bytes;
 };
 constexpr I8BackwardSpace i8_backward_space(int64_t rows, int64_t k, int64_t tokens, int type) {
     const int64_t padded = ceil_of(rows, kI8ChannelPad) * kI8ChannelPad;
     const int64_t coef = 4 * i8_limbs(type) * tokens * padded;
     const I8DxPlan plan = i8_dx_plan(rows, k, tokens, type);
     const int64_t dx = plan.splits > 1 ? 4 * plan.splits * tokens * k : 0;
-    const int64_t tiles = ceil_of(tokens, kI8Tiles[i8_tile_choice(rows, k, tokens, true, false)].tokens());
-    const int64_t parts = ceil_of(coef, 256) * 256, sums = parts + ceil_of(dx, 256) * 256;
-    return I8BackwardSpace{parts, sums, sums + 8 * rows * tiles};
+    const I8TileShape &tile = kI8Tiles[i8_tile_choice(rows, k, tokens, true, false)];
+    const int64_t tiles = ceil_of(tokens, tile.tokens()), one = i8_limbs(type) == 1 ? 1 : 0;
+    const int64_t blocks = one * tokens * ceil_of(rows, tile.wave_channels());
+    I8BackwardSpace s = {};
+    s.parts = ceil_of(coef, 256) * 256;
+    s.sums = s.parts + ceil_of(dx, 256) * 256;
+    s.exponents = s.sums + ceil_of(8 * rows * tiles, 256) * 256;
+    s.powers = s.exponents + ceil_of(blocks, 256) * 256;
+    s.bytes = s.powers + one * 4 * tokens;
+    return s;
 }
 constexpr int64_t gated_backward_workspace_bytes(int64_t rows, int64_t k, int64_t tokens, int type) {
     return i8_backward_space(rows, k, tokens, type).bytes;
