@@ -18,8 +18,8 @@ def loom(device):
 
 
 # (channels, k, tokens) that reach tiles of 32 x 32, 64 x 32, 64 x 64, 128 x 64, 64 x 128, 128 x 128, 128 x 256 and
-# 256 x 256 (channels x tokens) for the product or the gated projection, and of 32 x 32 and 32 x 64 whose waves split k,
-# with rows of k that end inside a step
+# 256 x 256 (channels x tokens) for the product or the gated projection, and of 32 x 32 whose waves split k, most with
+# one whole step of k and one that is partly filled (test_gpu_i8_ffn_rings: every tile of each operator, longer rows)
 SIZES = [(33, 132, 17), (500, 4100, 21), (500, 4100, 60), (100, 128, 33), (100, 60, 20), (33, 132, 4100), (8200, 132, 33), (16400, 132, 33), (4096, 1024, 512), (16400, 132, 65),
          (16400, 132, 200), (16400, 132, 257), (33, 132, 9), (4100, 132, 9), (4100, 132, 33), (16400, 132, 9),
          (200, 132, 4100), (8200, 132, 65), (11000, 132, 129), (2048, 2176, 2048)]
