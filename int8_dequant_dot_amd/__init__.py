@@ -119,8 +119,10 @@ def launch_config_invoke(token: int, workload) -> dict:
 
 # ------------------------------------------------------------------ tensor helpers
 
-# the current stream's handle without a Stream object around it (1.1 us a call)
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the current stream's handle without a Stream object around it (1.1 us a call), where this torch has that call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
 
 def _target(t: torch.Tensor, name: str):
     """The current HIP device index and its current stream: the C ABI launches
