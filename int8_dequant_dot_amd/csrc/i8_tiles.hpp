@@ -19,7 +19,7 @@ __device__ __forceinline__ void load_to_lds(int4v rsrc, int voff, int soff, int 
         "buffer_load_dwordx4 %1, %2, %3 offen lds"
         :
         : "s"(at), "v"(voff), "s"(rsrc), "s"(soff)
-        : "memory");
+        : "memory", "m0");
 }
 template <int LEFT>
 __device__ __forceinline__ void wait_loads() {
