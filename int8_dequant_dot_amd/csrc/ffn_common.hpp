@@ -62,11 +62,6 @@ __device__ __forceinline__ void store4_each(void *out, int type, int64_t at, int
     else if (type == LOOM_F16) store4_each_as((_Float16 *)out + at, by, left, whole, live, y);
     else store4_each_as((__bf16 *)out + at, by, left, whole, live, y);
 }
-__device__ __forceinline__ float load1(const void *in, int type, int64_t at) {
-    if (type == LOOM_F32) return ((const float *)in)[at];
-    if (type == LOOM_F16) return (float)((const _Float16 *)in)[at];
-    return (float)((const __bf16 *)in)[at];
-}
 template <typename T>
 __device__ __forceinline__ void load4_as(const T *from, int64_t left, bool whole, float (&y)[4]) {
     typedef T V __attribute__((ext_vector_type(4)));
