@@ -92,9 +92,10 @@ __device__ __forceinline__ void store1(void *out, int type, int64_t at, float y)
 __device__ __forceinline__ float normal_cdf(float g) { return 0.5f * erfcf(g * -0.70710678118654752f); }
 
 // 1 / (1 + exp(-z)) with the exponential and the reciprocal of the hardware,
-// each within one unit in the last place; the exponent -z log2(e) carries one
-// rounding more, an error of |z| 2^-24 of the exponential.  (The library's expf
-// and a rounded quotient took 40 instructions, 8 % of a 4096-token projection.)
+// each within one unit in the last place; the exponent -z log2(e) carries the
+// product's rounding and the constant's (0.23 of half a step more), an error of
+// 1.23 |z| 2^-24 of the exponential.  (The library's expf and a rounded quotient
+// took 40 instructions, 8 % of a 4096-token projection.)
 // exp overflows to infinity for z < -128 ln 2, where the result is 0.
 __device__ __forceinline__ float sigmoid(float z) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));

@@ -544,9 +544,12 @@ constexpr int64_t i8_dx_steps(int64_t rows) { return 2 * ceil_of(rows, kI8Channe
 
 // The shape and the number of parts with the least estimated time, as
 // i8_tile_choice estimates it: a step of r workgroups a CU takes the longest of
-// 0.4 us (0.3 for the smallest shape), its bytes at 58 KB/us and its products at 7 M operations/us (the
-// conversions of the weights included); parts cost their traffic at 5 TB/s and a
-// launch.  The 256-token shape is for one limb: its LDS holds no ring of more.
+// 0.4 us (0.3 for the smallest shape), its bytes at 58 KB/us and its products at
+// 7 M operations/us (the conversions of the weights included); parts cost their
+// traffic at 5 TB/s and a launch.  The products' rate is one for all shapes, to
+// rank them, and above what is measured: 256 x 256 reaches 5.4 M operations/us,
+// 256 x 128 3.9 M.  The 256-token shape is for one limb: the fragments of two
+// would take the 256 registers that the sums leave.
 constexpr I8DxPlan i8_dx_plan(int64_t rows, int64_t k, int64_t tokens, int type) {
     const int limbs = i8_limbs(type);
     I8DxPlan best{2, 1, 0};
