@@ -306,10 +306,11 @@ __global__ __launch_bounds__(256) void token_powers_kernel(uint16_t *coef, int64
 // one limb, while the products of the fragment before run: 8 conversions and 4 byte
 // permutes, or 2 exclusive ors, 4 byte permutes and 4 subtractions, for XT * LIMBS
 // products.
-// 2048 tokens x 28672 channels x k 8192 in tiles of 256 x 256: 1.40 to 1.45 ms (1.3
-// to 1.4 PFLOP/s), the matrix cores 64 % busy at the clock their power leaves; with
-// waves of 128 x 128, which convert every weight fragment twice, 1.55 ms; without
-// the conversions it would take 1.3 ms, without its loads 1.2.
+// 2048 tokens x 28672 channels x k 8192 in tiles of 256 x 256, one limb: 1.38 to 1.52
+// ms (1.3 to 1.4 PFLOP/s), the matrix cores 66 % busy at the clock their power leaves.
+// With bfloat16's conversions, at 1.40 to 1.45 ms: waves of 128 x 128, which convert
+// every weight fragment twice, took 1.55 ms; without the conversions it would have
+// taken 1.3 ms, without its loads 1.2.
 template <int SHAPE, int LIMBS_>
 struct DxConfig {
     static constexpr I8DxShape kShape = kI8Dx[SHAPE];

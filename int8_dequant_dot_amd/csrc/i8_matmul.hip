@@ -24,8 +24,8 @@ namespace {
 // 4 v + (l >> 2 & 3); a quad's four lanes hold the four segments of one output.
 // The matrix cores do 4 times the useful products, a tenth of their time here;
 // in exchange the stream needs no LDS and every load reads whole lines.
-// Memory bounds it: one token x 16384 x 8192 takes 21 us (6.3 TB/s), the gated
-// unit x 28672 x 8192 69 us (6.8 TB/s).
+// Memory bounds it: one token x 16384 x 8192 takes 21.5 us (6.2 TB/s), the gated
+// unit x 28672 x 8192 70 us (6.8 TB/s).
 template <int VG>
 struct StreamRecord {
     int4v a[4], b[VG];

@@ -548,7 +548,7 @@ constexpr int64_t i8_dx_steps(int64_t rows) { return 2 * ceil_of(rows, kI8Channe
 // 7 M operations/us (the conversions of the weights included); parts cost their
 // traffic at 5 TB/s and a launch.  The products' rate is one for all shapes, to
 // rank them, and above what is measured: 256 x 256 reaches 5.4 M operations/us,
-// 256 x 128 3.9 M.  The 256-token shape is for one limb: the fragments of two
+// 256 x 128 3.9 to 4.3 M.  The 256-token shape is for one limb: the fragments of two
 // would take the 256 registers that the sums leave.
 constexpr I8DxPlan i8_dx_plan(int64_t rows, int64_t k, int64_t tokens, int type) {
     const int limbs = i8_limbs(type);
