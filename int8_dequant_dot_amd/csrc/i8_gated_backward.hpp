@@ -17,8 +17,8 @@
 // cost of one limb.  Its exponents have the range of one power of two for each
 // token: float16 is full down to 2^-20 of the token's largest coefficient, and
 // what is below is off by at most 2^-30 of that coefficient.  All sums are f32.
-// (One bfloat16 limb was as fast, and its rounding as large as d_x's own: 0.0023 of
-// d_x against 0.0017.  Two would double d_x's products.)
+// (One bfloat16 limb made the whole 2 to 4 % faster, and its rounding was as large as
+// d_x's own: 0.0023 of d_x against 0.0017.  Two would double d_x's products.)
 #pragma once
 
 #include <algorithm>
@@ -450,7 +450,7 @@ struct DxLoop {
         barrier();
         DxFragments<C> f0, f1;
         each_index<kReads>([&](auto r) { read<decltype(r)::value>(f0, 0, 0); });
-        uint32_t ready[2][4];  // the fragment in use, and the next, as bfloat16
+        uint32_t ready[2][4];  // the fragment in use, and the next, widened
         each_index<4>([&](auto j) { ready[0][decltype(j)::value] = pair<decltype(j)::value>(f0.a[0]); });
         // Half a step: the products of f, while the next half's fragments are read
         // into g and converted.
