@@ -98,6 +98,12 @@ typedef struct loom_launch_config {
  *   "quantize_rows"   (rows, cols)
  *   "i8_matmul", "i8_gated_projection" (rows, k, tokens)
  *   "i8_gated_projection_backward" (rows, k, tokens): its first kernel
+ *   "route_experts" (tokens, experts, groups, top_k)
+ *   "route_experts_backward" (tokens, experts, 1, top_k)
+ *   "group_routes"    (pairs, experts), pairs = tokens * routes
+ *   "i4_matmul"       (rows, k, tokens, group)
+ *   "i4_expert_matmul", "i4_expert_gated_projection"
+ *                     (rows, k, pairs, group, experts)
  * lookup: LOOM_ERR_NULL if a pointer is NULL, LOOM_ERR_UNKNOWN_EXPORT if no
  * kernel has that name.  The token stays valid for the life of the process. */
 int loom_launch_config_lookup(const char *export_name, uint32_t *token);
@@ -419,6 +425,153 @@ int loom_i8_gated_projection_backward(const int32_t *w_gate, const float *gate_s
                                       int64_t k, int64_t tokens, int act, const void *d_out, int type,
                                       int64_t d_stride, void *d_x, float *d_gate_scale, float *d_up_scale,
                                       void *workspace, int64_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * A layer of experts with 4-bit weights.  loom_route_experts chooses each    *
+ * token's experts, loom_group_routes puts the routes in the order of their   *
+ * experts, the loom_i4_expert_ products take each expert's rows together, and *
+ * loom_routed_combine (its ids the slots, its payload the last product's     *
+ * rows) brings them back to the tokens.                                      *
+ * ------------------------------------------------------------------------ */
+
+/* Scores of experts: exp(l) / sum exp(l) over a token's experts; 1 / (1 + exp(-l)). */
+typedef enum loom_score { LOOM_SOFTMAX = 0, LOOM_SIGMOID = 1 } loom_score;
+
+/* ------------------------------------------------------------------------ *
+ * Routing of tokens to experts.  With l a token's logits, s their scores    *
+ * and c the choices, s + bias or, without a bias, l:                        *
+ *  - the experts are `groups` runs of experts / groups neighbours; a group's *
+ *    value is its largest choice (group_top 1), or the sum of its two largest *
+ *    (group_top 2; without a bias, of its two largest scores).  Only the     *
+ *    top_groups groups of the largest values stay.                          *
+ *  - ids: the top_k experts of the largest choices among them, falling; ties *
+ *    go to the lower group and the lower expert.                            *
+ *  - weights: scale * s[ids], or scale * s[ids] / sum s[ids] where           *
+ *    renormalize is not 0 (the bias only chooses).                          *
+ * An expert whose logit or choice is -infinity is never chosen; where fewer  *
+ * than top_k are left, the rest of ids is -1 with weight 0 (a missing route  *
+ * of loom_group_routes and loom_routed_combine).  A token that has a NaN or  *
+ * +infinity among its logits, or a NaN among the choices of experts whose    *
+ * logit is not -infinity, gets ids 0 .. top_k - 1 and weights NaN.           *
+ * Choices that are computed are computed and compared in 64 bits, weights    *
+ * in f32; a ratio of renormalised weights stays exact where the scores       *
+ * themselves vanish.                                                        *
+ *   logits     : type[tokens], rows row_stride >= experts elements apart     *
+ *                (LOOM_ERR_SHAPE), device, aligned to its element           *
+ *   tokens     : 0 .. 2^31 - 1; 4 * tokens * row_stride must fit in an int64 *
+ *   experts    : 1 .. 1024; groups: 1 .. 64, a divisor of experts            *
+ *                (LOOM_ERR_SHAPE); top_groups: 1 .. groups                  *
+ *   top_k      : 1 .. 64, at most top_groups * experts / groups              *
+ *                (LOOM_ERR_SHAPE)                                           *
+ *   bias       : f32[experts], device, or NULL                              *
+ *   ids        : int32[tokens][top_k]; weights : f32[tokens][top_k]          *
+ * ------------------------------------------------------------------------ */
+int loom_route_experts(const void *logits, int type, int64_t tokens, int64_t experts, int64_t row_stride, int score,
+                       const float *bias, int64_t groups, int64_t top_groups, int64_t group_top, int64_t top_k,
+                       int renormalize, float scale, int32_t *ids, float *weights, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Gradient of the routing weights with respect to the logits, the choice     *
+ * held.  With d = scale * d_weights over a token's routes i, at their experts: *
+ *     softmax:      d_l[j] = s_j (d_j - sum_i s_i d_i), d_j = 0 elsewhere    *
+ *     sigmoid:      d_l[i] = d_i s_i (1 - s_i)                               *
+ *     renormalised, w_i = s_i / sum s: d_l[i] = w_i (d_i - sum_j w_j d_j),   *
+ *                   for a sigmoid times 1 - s_i                             *
+ * in f32, rounded once to the type of the logits; every other d_l is 0.  A   *
+ * route whose id is outside [0, experts) takes no part (and its d_weights is *
+ * not read); an expert that is named twice takes the sum of its terms in     *
+ * route order.  A token without routes gets zeros.                          *
+ *   logits, ids, d_weights : as there, the logits of the forward pass        *
+ *   d_logits   : type[tokens], rows d_stride >= experts elements apart       *
+ * ------------------------------------------------------------------------ */
+int loom_route_experts_backward(const void *logits, int type, int64_t tokens, int64_t experts, int64_t row_stride,
+                                int score, int64_t top_k, int renormalize, float scale, const int32_t *ids,
+                                const float *d_weights, void *d_logits, int64_t d_stride, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Routes in the order of their experts.  Route p = token * routes + i leads  *
+ * to expert ids[p]; the routes of one expert keep their order.               *
+ *     slots[p]   = the place of route p, or -1 where ids[p] is no expert     *
+ *     rows[at]   = the token of the route at that place, -1 past the last    *
+ *     offsets[e] = the first place of expert e; offsets[experts] = how many  *
+ *   ids       : int32[tokens][routes], device                               *
+ *   tokens, routes : tokens * routes < 2^31, routes <= 2^20                  *
+ *   experts   : 1 .. 1024                                                   *
+ *   slots, rows : int32[tokens * routes]; offsets : int32[experts + 1]       *
+ *               (written also where there are no tokens)                    *
+ *   workspace : device memory, 4-byte aligned, of at least the bytes that    *
+ *               loom_group_routes_workspace gives for the same sizes         *
+ *               (LOOM_ERR_RANGE; it may be NULL where that is 0)            *
+ * ------------------------------------------------------------------------ */
+int loom_group_routes_workspace(int64_t tokens, int64_t routes, int64_t experts, int64_t *bytes);
+int loom_group_routes(const int32_t *ids, int64_t tokens, int64_t routes, int64_t experts, int32_t *slots, int32_t *rows,
+                      int32_t *offsets, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * Matrix product of int8 activations with 4-bit weights that have a scale    *
+ * for each channel and group of k.                                          *
+ *     acc[t][n][g] = sum of w[n][i] * x[t][i] over group g     (exact, int32) *
+ *     out[t][n] = (sum_g scale[n][g] * f32(acc[t][n][g])) * x_scale[t] + bias[n] *
+ * in f32 (the sum over groups in a fixed order), rounded once to the output  *
+ * type; a NULL x_scale or bias leaves its operation out.                    *
+ * Packed 4-bit weights: two's complement, 32 neighbours of k in 16 bytes;    *
+ * byte b of them holds element b in its low four bits and element 16 + b in  *
+ * its high four.                                                            *
+ *   w          : int32[rows][k/8], device, 16-byte aligned                  *
+ *   w_scale    : scale_type[rows][ceil(k / group)], device                  *
+ *   scale_type : a loom_type                                                *
+ *   group      : a power of two (LOOM_ERR_SHAPE), 32 .. 2^17 (LOOM_ERR_RANGE); *
+ *                a last group may be shorter, one of k or more is one scale  *
+ *                a channel                                                  *
+ *   x          : int32[tokens][k/4] packed int8 activations, device,         *
+ *                16-byte aligned                                            *
+ *   x_scale    : f32[tokens], device, or NULL (= 1)                         *
+ *   bias       : f32[rows], device, or NULL (= 0)                           *
+ *   rows       : channels, 0 <= rows < 2^31                                 *
+ *   k          : k % 32 == 0 (LOOM_ERR_SHAPE), 0 <= k <= 131040             *
+ *   tokens     : 0 <= tokens < 2^31; LOOM_ERR_RANGE also when the grid      *
+ *                would reach 2^32 work-items, as loom_launch_config_invoke  *
+ *                reports for (rows, k, tokens, group)                       *
+ *   out        : type[tokens], rows out_stride >= rows elements apart       *
+ *                (LOOM_ERR_SHAPE), device, aligned to its element;          *
+ *                4 * tokens * out_stride must fit in an int64               *
+ * ------------------------------------------------------------------------ */
+int loom_i4_matmul(const int32_t *w, const void *w_scale, int scale_type, int64_t group, const int32_t *x,
+                   const float *x_scale, const float *bias, int64_t rows, int64_t k, int64_t tokens, void *out,
+                   int type, int64_t out_stride, void *stream);
+
+/* ------------------------------------------------------------------------ *
+ * The same product for experts: routed row p, offsets[e] <= p <              *
+ * offsets[e + 1], is row index[p] of x times the weights of expert e.        *
+ *     out[p][n] = loom_i4_matmul's for w[e], w_scale[e], bias[e], x[index[p]] *
+ * Rows of out that belong to no expert are left as they were.  offsets may   *
+ * name any rows: only those within [0, pairs) count, and an expert whose     *
+ * offsets fall has none; rows that several experts claim have no defined     *
+ * value.  A row whose index is outside [0, x_rows) becomes NaN.              *
+ *   w          : int32[experts][rows][k/8], w_scale : scale_type[experts]    *
+ *                [rows][ceil(k / group)], bias : f32[experts][rows] or NULL   *
+ *   x          : int32[x_rows][k/4], x_scale : f32[x_rows] or NULL           *
+ *   index      : int32[pairs], device, or NULL (row p of x)                 *
+ *   x_rows     : at least 1, and pairs without an index (LOOM_ERR_SHAPE)     *
+ *   offsets    : int32[experts + 1], device                                 *
+ *   experts    : 1 .. 1024                                                  *
+ *   pairs      : routed rows, 0 <= pairs < 2^31, and the grid as above, of   *
+ *                (rows, k, pairs, group, experts)                           *
+ *   out        : type[pairs], rows out_stride apart                         *
+ * ------------------------------------------------------------------------ */
+int loom_i4_expert_matmul(const int32_t *w, const void *w_scale, int scale_type, int64_t group, const int32_t *x,
+                          const float *x_scale, int64_t x_rows, const int32_t *index, const int32_t *offsets,
+                          const float *bias, int64_t experts, int64_t rows, int64_t k, int64_t pairs, void *out,
+                          int type, int64_t out_stride, void *stream);
+
+/* Gated projection of experts: act(g) * u with g and u the products above (no
+ * bias) for the two weights, in f32, rounded once.  act is a loom_activation,
+ * anything else LOOM_ERR_RANGE. */
+int loom_i4_expert_gated_projection(const int32_t *w_gate, const void *gate_scale, const int32_t *w_up,
+                                    const void *up_scale, int scale_type, int64_t group, const int32_t *x,
+                                    const float *x_scale, int64_t x_rows, const int32_t *index, const int32_t *offsets,
+                                    int64_t experts, int64_t rows, int64_t k, int64_t pairs, int act, void *out,
+                                    int type, int64_t out_stride, void *stream);
 
 #ifdef __cplusplus
 }

@@ -48,12 +48,25 @@ _lib.loom_i8_gated_projection.argtypes = [_p, _p, _p, _p, _p, _p, _i64, _i64, _i
 _lib.loom_i8_gated_projection_backward_workspace.argtypes = [_i64, _i64, _i64, ctypes.c_int, _p]
 _lib.loom_i8_gated_projection_backward.argtypes = [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, ctypes.c_int, _p,
                                                    ctypes.c_int, _i64, _p, _p, _p, _p, _i64, _p]
+_int, _float = ctypes.c_int, ctypes.c_float
+_lib.loom_route_experts.argtypes = [_p, _int, _i64, _i64, _i64, _int, _p, _i64, _i64, _i64, _i64, _int, _float, _p, _p,
+                                    _p]
+_lib.loom_route_experts_backward.argtypes = [_p, _int, _i64, _i64, _i64, _int, _i64, _int, _float, _p, _p, _p, _i64, _p]
+_lib.loom_group_routes_workspace.argtypes = [_i64, _i64, _i64, _p]
+_lib.loom_group_routes.argtypes = [_p, _i64, _i64, _i64, _p, _p, _p, _p, _i64, _p]
+_lib.loom_i4_matmul.argtypes = [_p, _p, _int, _i64, _p, _p, _p, _i64, _i64, _i64, _p, _int, _i64, _p]
+_lib.loom_i4_expert_matmul.argtypes = [_p, _p, _int, _i64, _p, _p, _i64, _p, _p, _p, _i64, _i64, _i64, _i64, _p, _int,
+                                       _i64, _p]
+_lib.loom_i4_expert_gated_projection.argtypes = [_p, _p, _p, _p, _int, _i64, _p, _p, _i64, _p, _p, _i64, _i64, _i64,
+                                                 _i64, _int, _p, _int, _i64, _p]
 for _name in ("loom_launch_config_lookup", "loom_launch_config_invoke", "loom_copy_f32", "loom_row_sum_tiles",
               "loom_row_sums", "loom_segment_sums", "loom_segment_sums_noalloc", "loom_i8_dequant_dot",
               "loom_packed_dot",
               "loom_sum_guarded_rows", "loom_routed_combine", "loom_quantize_rows", "loom_i8_matmul",
               "loom_i8_gated_projection", "loom_i8_gated_projection_backward_workspace",
-              "loom_i8_gated_projection_backward"):
+              "loom_i8_gated_projection_backward", "loom_route_experts", "loom_route_experts_backward",
+              "loom_group_routes_workspace", "loom_group_routes", "loom_i4_matmul", "loom_i4_expert_matmul",
+              "loom_i4_expert_gated_projection"):
     getattr(_lib, _name).restype = ctypes.c_int
 
 # status codes (include/loom.h)
@@ -61,11 +74,13 @@ OK, ERR_NULL, ERR_RANGE, ERR_ALIGN, ERR_SHAPE, ERR_UNKNOWN_EXPORT, ERR_TOKEN, ER
 
 EXPORTS = ("copy_f32", "row_sum_tiles", "row_sums", "segment_sums", "i8_dequant_dot", "packed_dot",
            "sum_guarded_rows", "routed_combine", "quantize_rows", "i8_matmul", "i8_gated_projection",
-           "i8_gated_projection_backward")
+           "i8_gated_projection_backward", "route_experts", "route_experts_backward", "group_routes", "i4_matmul",
+           "i4_expert_matmul", "i4_expert_gated_projection")
 
 # loom_type and loom_activation (include/loom.h)
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+SCORES = {"softmax": 0, "sigmoid": 1}  # loom_score
 
 
 class LoomError(RuntimeError):
@@ -484,3 +499,206 @@ def pack_int8(t: torch.Tensor) -> torch.Tensor:
     if t.shape[-1] == 0:
         return torch.empty(*t.shape[:-1], 0, dtype=torch.int32, device=t.device)
     return t.view(torch.int32)
+
+
+# ------------------------------------------------------------------ experts with 4-bit weights
+
+def _score(score: str) -> int:
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {', '.join(SCORES)}, got {score!r}")
+    return SCORES[score]
+
+
+def _logits(logits, device):
+    """Checks router logits [tokens][experts] -> (loom_type, tokens, experts, row stride)."""
+    kind = _type(logits.dtype, "logits")
+    _require(logits.dim() == 2, "logits must be [tokens][experts]")
+    tokens, experts = logits.shape
+    return kind, tokens, experts, _rows_of(logits, logits.dtype, tokens, experts, "logits", device)
+
+
+def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None,
+                  groups: int = 1, top_groups: int = 1, group_top: int = 2, renormalize: bool = True,
+                  scale: float = 1.0, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None):
+    """logits [tokens][experts] f32, f16 or bf16 (rows may be strided) -> (ids int32 [tokens][top_k], weights f32
+    [tokens][top_k]): the experts of the largest choices, score + bias (f32 [experts]) or the logit without a bias,
+    among the top_groups best of ``groups`` runs of experts, and scale * score, over their sum if renormalize.
+
+    score: 'softmax' or 'sigmoid'.  group_top: how many of a group's largest choices make its value, 1 or 2.
+    Experts whose logit is -inf are never chosen; ids that are missing for that are -1, with weight 0."""
+    device, stream = _target(logits, "logits")
+    kind, tokens, experts, stride = _logits(logits, device)
+    code = _score(score)
+    _buffer(bias, torch.float32, experts, "bias", device, optional=True)
+    if ids is None:
+        ids = torch.empty(tokens, max(top_k, 0), dtype=torch.int32, device=logits.device)
+    _buffer(ids, torch.int32, tokens * top_k, "ids", device)
+    if weights is None:
+        weights = torch.empty(tokens, max(top_k, 0), dtype=torch.float32, device=logits.device)
+    _buffer(weights, torch.float32, tokens * top_k, "weights", device)
+    _check(_lib.loom_route_experts(_ptr(logits), kind, tokens, experts, stride, code, _ptr(bias), groups, top_groups,
+                                   group_top, top_k, int(renormalize), scale, _ptr(ids), _ptr(weights), stream),
+           "route_experts")
+    return ids, weights
+
+
+def route_experts_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor, score: str = "softmax",
+                           renormalize: bool = True, scale: float = 1.0,
+                           d_logits: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of route_experts' weights for d_weights f32 [tokens][top_k], with its logits and ids
+    -> d_logits [tokens][experts] of the logits' type (rows of a given ``d_logits`` may be strided)."""
+    device, stream = _target(logits, "logits")
+    kind, tokens, experts, stride = _logits(logits, device)
+    code = _score(score)
+    _dev(ids, torch.int32, "ids", device)
+    _dev(d_weights, torch.float32, "d_weights", device)
+    _require(ids.dim() == 2 and ids.shape[0] == tokens and ids.is_contiguous(), "ids must be a contiguous [tokens][top_k] tensor")
+    _require(d_weights.shape == ids.shape and d_weights.is_contiguous(), "d_weights must be contiguous, shaped as ids")
+    if d_logits is None:
+        d_logits = torch.empty(tokens, experts, dtype=logits.dtype, device=logits.device)
+    d_stride = _rows_of(d_logits, logits.dtype, tokens, experts, "d_logits", device)
+    _check(_lib.loom_route_experts_backward(_ptr(logits), kind, tokens, experts, stride, code, ids.shape[1],
+                                            int(renormalize), scale, _ptr(ids), _ptr(d_weights), _ptr(d_logits),
+                                            d_stride, stream), "route_experts_backward")
+    return d_logits
+
+
+def group_routes_workspace(tokens: int, routes: int, experts: int) -> int:
+    """Bytes of workspace that group_routes needs for these sizes."""
+    n = ctypes.c_int64()
+    _check(_lib.loom_group_routes_workspace(tokens, routes, experts, ctypes.byref(n)), "group_routes_workspace")
+    return n.value
+
+
+def group_routes(ids: torch.Tensor, experts: int, slots: torch.Tensor | None = None, rows: torch.Tensor | None = None,
+                 offsets: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """ids int32 [tokens][routes] -> (slots int32 [tokens][routes], rows int32 [tokens * routes], offsets int32
+    [experts + 1]): where each route stands in the order of experts (-1: its id is no expert), whose token stands at
+    each place (-1 past the last), and where each expert's places begin.
+
+    slots are the ids that routed_combine takes for the rows of the experts' products.
+    workspace: a uint8 buffer of group_routes_workspace bytes, 4-byte aligned (made here if None)."""
+    device, stream = _target(ids, "ids")
+    _dev(ids, torch.int32, "ids", device)
+    _require(ids.dim() == 2 and ids.is_contiguous(), "ids must be a contiguous [tokens][routes] tensor")
+    tokens, routes = ids.shape
+    need = group_routes_workspace(tokens, routes, experts)
+    if slots is None:
+        slots = torch.empty(tokens, routes, dtype=torch.int32, device=ids.device)
+    _buffer(slots, torch.int32, tokens * routes, "slots", device)
+    if rows is None:
+        rows = torch.empty(tokens * routes, dtype=torch.int32, device=ids.device)
+    _buffer(rows, torch.int32, tokens * routes, "rows", device)
+    if offsets is None:
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+    _buffer(offsets, torch.int32, experts + 1, "offsets", device)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
+    _buffer(workspace, torch.uint8, need, "workspace", device, optional=need == 0)
+    _check(_lib.loom_group_routes(_ptr(ids), tokens, routes, experts, _ptr(slots), _ptr(rows), _ptr(offsets),
+                                  _ptr(workspace), need, stream), "group_routes")
+    return slots, rows, offsets
+
+
+def _weights4(w, w_scale, group, lead, device, w_name, s_name):
+    """Checks packed 4-bit weights [rows][k/8] (experts first where lead is 3) and their scales [..][rows][groups]
+    -> (k, the scales' loom_type)."""
+    _dev(w, torch.int32, w_name, device)
+    shape = "[rows][k/8]" if lead == 2 else "[experts][rows][k/8]"
+    if w.dim() != lead or not w.is_contiguous():
+        raise ValueError(f"{w_name} must be a contiguous {shape} tensor")
+    kind = _type(getattr(w_scale, "dtype", None), s_name)
+    _require(group >= 1, "group must be positive")
+    k = 8 * w.shape[-1]
+    count = w.shape[0] * (w.shape[1] if lead == 3 else 1)
+    _buffer(w_scale, w_scale.dtype, count * -(-k // group), s_name, device)
+    return k, kind
+
+
+def _activations4(x, x_scale, k, device, w_name):
+    """Checks packed activations [tokens][k/4] or [k/4] and their scales -> tokens."""
+    return _activations(x, x_scale, k // 4, device, w_name)
+
+
+def i4_matmul(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor | None = None,
+              bias: torch.Tensor | None = None, group: int = 128, dtype: torch.dtype = torch.bfloat16,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """w int32 [rows][k/8] (packed 4-bit, see pack_int4), w_scale f32, f16 or bf16 [rows][ceil(k / group)], x int32
+    [tokens][k/4] or [k/4] (packed int8), x_scale f32 [tokens], bias f32 [rows] -> out [tokens][rows] of ``dtype`` (or
+    of ``out``, whose rows may be strided).  group: a power of two, at least 32; k % 32 == 0; w and x 16-byte aligned."""
+    device, stream = _target(w, "w")
+    k, scales = _weights4(w, w_scale, group, 2, device, "w", "w_scale")
+    rows = w.shape[0]
+    tokens = _activations4(x, x_scale, k, device, "w")
+    _buffer(bias, torch.float32, rows, "bias", device, optional=True)
+    out, kind, stride = _result(out, dtype, tokens, rows, w, device)
+    _check(_lib.loom_i4_matmul(_ptr(w), _ptr(w_scale), scales, group, _ptr(x), _ptr(x_scale), _ptr(bias), rows, k, tokens,
+                               _ptr(out), kind, stride, stream), "i4_matmul")
+    return out
+
+
+def _routed(x, x_scale, index, offsets, experts, k, device, w_name):
+    """Checks the activations, index and offsets of an experts' product -> (routed rows, rows of x)."""
+    x_rows = _activations4(x, x_scale, k, device, w_name)
+    _buffer(offsets, torch.int32, experts + 1, "offsets", device)
+    if index is None:
+        return x_rows, x_rows
+    _dev(index, torch.int32, "index", device)
+    _require(index.is_contiguous(), "index must be contiguous")
+    return index.numel(), x_rows
+
+
+def i4_expert_matmul(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor | None,
+                     offsets: torch.Tensor, index: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                     group: int = 128, dtype: torch.dtype = torch.bfloat16,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """i4_matmul for experts: w int32 [experts][rows][k/8], w_scale [experts][rows][ceil(k / group)], bias f32
+    [experts][rows]; routed rows offsets[e] .. offsets[e + 1] - 1 (group_routes) are rows index[p] of x (or rows p of x,
+    without an index) times the weights of expert e -> out [routed rows][rows].
+
+    Rows of out that belong to no expert are not written: hand in an ``out`` to know what they hold."""
+    device, stream = _target(w, "w")
+    k, scales = _weights4(w, w_scale, group, 3, device, "w", "w_scale")
+    experts, rows = w.shape[:2]
+    pairs, x_rows = _routed(x, x_scale, index, offsets, experts, k, device, "w")
+    _buffer(bias, torch.float32, experts * rows, "bias", device, optional=True)
+    out, kind, stride = _result(out, dtype, pairs, rows, w, device)
+    _check(_lib.loom_i4_expert_matmul(_ptr(w), _ptr(w_scale), scales, group, _ptr(x), _ptr(x_scale), x_rows, _ptr(index),
+                                      _ptr(offsets), _ptr(bias), experts, rows, k, pairs, _ptr(out), kind, stride,
+                                      stream), "i4_expert_matmul")
+    return out
+
+
+def i4_expert_gated_projection(w_gate: torch.Tensor, gate_scale: torch.Tensor, w_up: torch.Tensor,
+                               up_scale: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor | None,
+                               offsets: torch.Tensor, index: torch.Tensor | None = None, act: str = "silu",
+                               group: int = 128, dtype: torch.dtype = torch.bfloat16,
+                               out: torch.Tensor | None = None) -> torch.Tensor:
+    """act(x w_gate^T) * (x w_up^T) for experts, operands as in i4_expert_matmul for both weights -> out [routed
+    rows][rows].  act: 'silu', 'gelu', 'gelu_tanh' or 'relu'."""
+    device, stream = _target(w_gate, "w_gate")
+    k, scales = _weights4(w_gate, gate_scale, group, 3, device, "w_gate", "gate_scale")
+    _, up_kind = _weights4(w_up, up_scale, group, 3, device, "w_up", "up_scale")
+    _require(w_up.shape == w_gate.shape, "w_up must be shaped as w_gate")
+    _require(up_kind == scales, "up_scale must have gate_scale's type")
+    experts, rows = w_gate.shape[:2]
+    pairs, x_rows = _routed(x, x_scale, index, offsets, experts, k, device, "w_gate")
+    code = _act(act)
+    out, kind, stride = _result(out, dtype, pairs, rows, w_gate, device)
+    _check(_lib.loom_i4_expert_gated_projection(_ptr(w_gate), _ptr(gate_scale), _ptr(w_up), _ptr(up_scale), scales, group,
+                                                _ptr(x), _ptr(x_scale), x_rows, _ptr(index), _ptr(offsets), experts, rows,
+                                                k, pairs, code, _ptr(out), kind, stride, stream),
+           "i4_expert_gated_projection")
+    return out
+
+
+def pack_int4(t: torch.Tensor) -> torch.Tensor:
+    """int8 values -8 .. 7 [..., k] (k % 32 == 0) as packed int32 [..., k/8] words, on the tensor's own device: of each
+    16 bytes, byte b holds element b of 32 in its low four bits and element 16 + b in its high four."""
+    _require(t.dtype == torch.int8 and t.shape[-1] % 32 == 0,
+             "pack_int4 needs an int8 tensor whose last dimension is a multiple of 32")
+    k = t.shape[-1]
+    if t.numel() == 0:
+        return torch.empty(*t.shape[:-1], k // 8, dtype=torch.int32, device=t.device)
+    halves = t.contiguous().view(torch.uint8).view(*t.shape[:-1], k // 32, 2, 16)
+    return ((halves[..., 0, :] & 15) | (halves[..., 1, :] << 4)).reshape(*t.shape[:-1], k // 2).view(torch.int32)

@@ -339,3 +339,189 @@ extern "C" int loom_i8_gated_projection_backward(const int32_t *w_gate, const fl
         return run(cfg, p, d_out, d_stride, d_x, d_gate_scale, d_up_scale, workspace, (hipStream_t)stream);
     });
 }
+
+namespace {
+
+bool known_score(int score) { return score == LOOM_SOFTMAX || score == LOOM_SIGMOID; }
+
+// The size checks shared by the router and its gradient.
+int route_sizes(loom::ExportId id, int64_t tokens, int64_t experts, int64_t groups, int64_t top_k, int type, int score,
+                int64_t stride, loom_launch_config *cfg) {
+    if (tokens < 0 || tokens > kMaxRows || !known_type(type) || !known_score(score)) return LOOM_ERR_RANGE;
+    if (experts < 1 || experts > loom::kRouteMaxExperts || groups < 1 || groups > loom::kRouteMaxGroups || top_k < 1 ||
+        top_k > loom::kRouteMaxTopK)
+        return LOOM_ERR_RANGE;
+    if (stride < experts || top_k > experts) return LOOM_ERR_SHAPE;
+    if (tokens > 0 && stride > (INT64_MAX / 4) / tokens) return LOOM_ERR_RANGE;
+    const int64_t w[4] = {tokens, experts, groups, top_k};
+    return loom::evaluate_launch(id, w, cfg);
+}
+
+}  // namespace
+
+extern "C" int loom_route_experts(const void *logits, int type, int64_t tokens, int64_t experts, int64_t row_stride,
+                                  int score, const float *bias, int64_t groups, int64_t top_groups, int64_t group_top,
+                                  int64_t top_k, int renormalize, float scale, int32_t *ids, float *weights,
+                                  void *stream) {
+    if (group_top < 1 || group_top > 2) return LOOM_ERR_RANGE;
+    loom_launch_config cfg;
+    if (int st = route_sizes(loom::kRouteExperts, tokens, experts, groups, top_k, type, score, row_stride, &cfg)) return st;
+    if (top_groups < 1 || top_groups > groups) return LOOM_ERR_RANGE;
+    if (experts % groups != 0 || top_k > top_groups * (experts / groups)) return LOOM_ERR_SHAPE;
+    if (tokens == 0) return LOOM_OK;
+    if (!logits || !ids || !weights) return LOOM_ERR_NULL;
+    if (misaligned(logits, element_size(type)) || misaligned(bias, 4) || misaligned(ids, 4) || misaligned(weights, 4))
+        return LOOM_ERR_ALIGN;
+    loom::RouteArgs a = {};
+    a.logits = logits, a.bias = bias, a.tokens = tokens, a.stride = row_stride;
+    a.type = type, a.score = score, a.experts = (int)experts, a.groups = (int)groups, a.top_groups = (int)top_groups;
+    a.group_top = (int)group_top, a.top_k = (int)top_k, a.renormalize = renormalize != 0, a.scale = scale;
+    a.ids = ids, a.weights = weights;
+    return launch([&] { return loom::launch_route_experts(cfg, a, (hipStream_t)stream); });
+}
+
+extern "C" int loom_route_experts_backward(const void *logits, int type, int64_t tokens, int64_t experts,
+                                           int64_t row_stride, int score, int64_t top_k, int renormalize, float scale,
+                                           const int32_t *ids, const float *d_weights, void *d_logits, int64_t d_stride,
+                                           void *stream) {
+    loom_launch_config cfg;
+    if (int st = route_sizes(loom::kRouteExpertsBackward, tokens, experts, 1, top_k, type, score, row_stride, &cfg))
+        return st;
+    if (d_stride < experts) return LOOM_ERR_SHAPE;
+    if (tokens > 0 && d_stride > (INT64_MAX / 4) / tokens) return LOOM_ERR_RANGE;
+    if (tokens == 0) return LOOM_OK;
+    if (!logits || !ids || !d_weights || !d_logits) return LOOM_ERR_NULL;
+    if (misaligned(logits, element_size(type)) || misaligned(ids, 4) || misaligned(d_weights, 4) ||
+        misaligned(d_logits, element_size(type)))
+        return LOOM_ERR_ALIGN;
+    loom::RouteArgs a = {};
+    a.logits = logits, a.tokens = tokens, a.stride = row_stride, a.type = type, a.score = score;
+    a.experts = (int)experts, a.groups = 1, a.top_groups = 1, a.group_top = 1, a.top_k = (int)top_k;
+    a.renormalize = renormalize != 0, a.scale = scale, a.ids = const_cast<int32_t *>(ids);
+    a.d_weights = d_weights, a.d_logits = d_logits, a.d_stride = d_stride;
+    return launch([&] { return loom::launch_route_experts_backward(cfg, a, (hipStream_t)stream); });
+}
+
+namespace {
+
+int group_sizes(int64_t tokens, int64_t routes, int64_t experts, loom_launch_config *cfg) {
+    if (tokens < 0 || tokens > kMaxRows || routes < 0 || routes > (int64_t(1) << 20) || tokens * routes > kMaxRows ||
+        experts < 1 || experts > loom::kGroupMaxExperts)
+        return LOOM_ERR_RANGE;
+    const int64_t w[2] = {tokens * routes, experts};
+    return loom::evaluate_launch(loom::kGroupRoutes, w, cfg);
+}
+
+}  // namespace
+
+extern "C" int loom_group_routes_workspace(int64_t tokens, int64_t routes, int64_t experts, int64_t *bytes) {
+    if (!bytes) return LOOM_ERR_NULL;
+    loom_launch_config cfg;
+    if (int st = group_sizes(tokens, routes, experts, &cfg)) return st;
+    *bytes = loom::group_workspace_bytes(tokens * routes, experts);
+    return LOOM_OK;
+}
+
+extern "C" int loom_group_routes(const int32_t *ids, int64_t tokens, int64_t routes, int64_t experts, int32_t *slots,
+                                 int32_t *rows, int32_t *offsets, void *workspace, int64_t workspace_bytes,
+                                 void *stream) {
+    loom_launch_config cfg;
+    if (int st = group_sizes(tokens, routes, experts, &cfg)) return st;
+    const int64_t pairs = tokens * routes, need = loom::group_workspace_bytes(pairs, experts);
+    if (workspace_bytes < need) return LOOM_ERR_RANGE;
+    if (!offsets || (pairs > 0 && (!ids || !slots || !rows)) || (need > 0 && !workspace)) return LOOM_ERR_NULL;
+    if (misaligned(ids, 4) || misaligned(slots, 4) || misaligned(rows, 4) || misaligned(offsets, 4) ||
+        misaligned(workspace, 4))
+        return LOOM_ERR_ALIGN;
+    const loom::GroupArgs a = {ids,   pairs, routes > 0 ? routes : 1, loom::group_part(pairs), (int)experts, slots,
+                               rows, offsets, (int32_t *)workspace};
+    return launch([&] { return loom::launch_group_routes(cfg, a, (hipStream_t)stream); });
+}
+
+namespace {
+
+// The size checks of the 4-bit products; experts 0 for the dense one.
+int i4_sizes(loom::ExportId id, int64_t rows, int64_t k, int64_t tokens, int64_t group, int64_t experts,
+             int scale_type, int type, int64_t stride, loom_launch_config *cfg) {
+    if (k < 0 || k > loom::kI4MaxK || rows < 0 || rows > kMaxRows || tokens < 0 || tokens > kMaxRows ||
+        !known_type(type) || !known_type(scale_type) || group < 32 || group > (int64_t(1) << 17))
+        return LOOM_ERR_RANGE;
+    if (id != loom::kI4Matmul && (experts < 1 || experts > loom::kI4MaxExperts)) return LOOM_ERR_RANGE;
+    if (k % 32 != 0 || (group & (group - 1)) != 0 || stride < rows) return LOOM_ERR_SHAPE;
+    if (tokens > 0 && stride > (INT64_MAX / 4) / tokens) return LOOM_ERR_RANGE;
+    const int64_t w[5] = {rows, k, tokens, group, experts};
+    return loom::evaluate_launch(id, w, cfg);
+}
+
+void i4_fill(loom::I4Product &p, int64_t rows, int64_t k, int64_t tokens, int64_t group, int64_t experts) {
+    p.rows = (int)rows, p.tokens = (int)tokens, p.chunks = (int)(k / 32);
+    p.groups = (int)loom::ceil_of(k, group), p.chunk_shift = __builtin_ctzll((uint64_t)group) - 5;
+    p.experts = (int)experts;
+}
+
+}  // namespace
+
+extern "C" int loom_i4_matmul(const int32_t *w, const void *w_scale, int scale_type, int64_t group, const int32_t *x,
+                              const float *x_scale, const float *bias, int64_t rows, int64_t k, int64_t tokens,
+                              void *out, int type, int64_t out_stride, void *stream) {
+    loom_launch_config cfg;
+    if (int st = i4_sizes(loom::kI4Matmul, rows, k, tokens, group, 0, scale_type, type, out_stride, &cfg)) return st;
+    if (rows == 0 || tokens == 0) return LOOM_OK;
+    if (!out || (k > 0 && (!w || !w_scale || !x))) return LOOM_ERR_NULL;
+    if (misaligned(w, 16) || misaligned(x, 16) || misaligned(w_scale, element_size(scale_type)) ||
+        misaligned(x_scale, 4) || misaligned(bias, 4) || misaligned(out, element_size(type)))
+        return LOOM_ERR_ALIGN;
+    loom::I4Product p = {};
+    i4_fill(p, rows, k, tokens, group, 1);
+    p.w = w, p.w_scale = w_scale, p.x = x, p.x_scale = x_scale, p.bias = bias, p.x_rows = tokens;
+    p.out = out, p.out_stride = out_stride;
+    return launch([&] { return loom::launch_i4_product(cfg, p, loom::kI4Dense, scale_type, type, (hipStream_t)stream); });
+}
+
+extern "C" int loom_i4_expert_matmul(const int32_t *w, const void *w_scale, int scale_type, int64_t group,
+                                     const int32_t *x, const float *x_scale, int64_t x_rows, const int32_t *index,
+                                     const int32_t *offsets, const float *bias, int64_t experts, int64_t rows,
+                                     int64_t k, int64_t pairs, void *out, int type, int64_t out_stride, void *stream) {
+    loom_launch_config cfg;
+    if (int st = i4_sizes(loom::kI4ExpertMatmul, rows, k, pairs, group, experts, scale_type, type, out_stride, &cfg))
+        return st;
+    if (x_rows < 0 || x_rows > kMaxRows) return LOOM_ERR_RANGE;
+    if (pairs > 0 && x_rows < (index ? 1 : pairs)) return LOOM_ERR_SHAPE;
+    if (rows == 0 || pairs == 0) return LOOM_OK;
+    if (!offsets || !out || (k > 0 && (!w || !w_scale || !x))) return LOOM_ERR_NULL;
+    if (misaligned(w, 16) || misaligned(x, 16) || misaligned(w_scale, element_size(scale_type)) ||
+        misaligned(x_scale, 4) || misaligned(index, 4) || misaligned(offsets, 4) || misaligned(bias, 4) ||
+        misaligned(out, element_size(type)))
+        return LOOM_ERR_ALIGN;
+    loom::I4Product p = {};
+    i4_fill(p, rows, k, pairs, group, experts);
+    p.w = w, p.w_scale = w_scale, p.x = x, p.x_scale = x_scale, p.bias = bias, p.index = index, p.offsets = offsets;
+    p.x_rows = x_rows, p.out = out, p.out_stride = out_stride;
+    return launch([&] { return loom::launch_i4_product(cfg, p, loom::kI4Routed, scale_type, type, (hipStream_t)stream); });
+}
+
+extern "C" int loom_i4_expert_gated_projection(const int32_t *w_gate, const void *gate_scale, const int32_t *w_up,
+                                               const void *up_scale, int scale_type, int64_t group, const int32_t *x,
+                                               const float *x_scale, int64_t x_rows, const int32_t *index,
+                                               const int32_t *offsets, int64_t experts, int64_t rows, int64_t k,
+                                               int64_t pairs, int act, void *out, int type, int64_t out_stride,
+                                               void *stream) {
+    if (!known_act(act)) return LOOM_ERR_RANGE;
+    loom_launch_config cfg;
+    if (int st = i4_sizes(loom::kI4ExpertGatedProjection, rows, k, pairs, group, experts, scale_type, type, out_stride,
+                          &cfg))
+        return st;
+    if (x_rows < 0 || x_rows > kMaxRows) return LOOM_ERR_RANGE;
+    if (pairs > 0 && x_rows < (index ? 1 : pairs)) return LOOM_ERR_SHAPE;
+    if (rows == 0 || pairs == 0) return LOOM_OK;
+    if (!offsets || !out || (k > 0 && (!w_gate || !w_up || !gate_scale || !up_scale || !x))) return LOOM_ERR_NULL;
+    if (misaligned(w_gate, 16) || misaligned(w_up, 16) || misaligned(x, 16) ||
+        misaligned(gate_scale, element_size(scale_type)) || misaligned(up_scale, element_size(scale_type)) ||
+        misaligned(x_scale, 4) || misaligned(index, 4) || misaligned(offsets, 4) || misaligned(out, element_size(type)))
+        return LOOM_ERR_ALIGN;
+    loom::I4Product p = {};
+    i4_fill(p, rows, k, pairs, group, experts);
+    p.w = w_gate, p.w_scale = gate_scale, p.w_up = w_up, p.up_scale = up_scale, p.x = x, p.x_scale = x_scale;
+    p.index = index, p.offsets = offsets, p.act = act, p.x_rows = x_rows, p.out = out, p.out_stride = out_stride;
+    return launch([&] { return loom::launch_i4_product(cfg, p, loom::kI4RoutedGated, scale_type, type, (hipStream_t)stream); });
+}

@@ -22,6 +22,12 @@ enum ExportId : uint32_t {
     kI8Matmul,
     kI8GatedProjection,
     kI8GatedBackward,
+    kRouteExperts,
+    kRouteExpertsBackward,
+    kGroupRoutes,
+    kI4Matmul,
+    kI4ExpertMatmul,
+    kI4ExpertGatedProjection,
     kExportCount
 };
 
@@ -607,6 +613,67 @@ constexpr int64_t gated_backward_workspace_bytes(int64_t rows, int64_t k, int64_
     return i8_backward_space(rows, k, tokens, type).bytes;
 }
 
+// The router and its gradient.  A token is held by 2^route_log_lanes lanes.
+constexpr int64_t kRouteMaxExperts = 1024, kRouteMaxTopK = 64, kRouteMaxGroups = 64;
+constexpr int kRouteWaves = 4;
+constexpr int route_log_lanes(int64_t tokens, int64_t experts, int64_t top_k) {
+    return experts <= 256 && top_k <= 16 && tokens >= 1024 ? 4 : 6;
+}
+struct RouteArgs {
+    const void *logits;      // type[tokens], rows stride elements apart
+    const float *bias;       // [experts] or NULL
+    int64_t tokens, stride;
+    int type, score, experts, groups, top_groups, group_top, top_k, renormalize;
+    float scale;
+    int32_t *ids;            // [tokens][top_k]; read by the gradient
+    float *weights;          // [tokens][top_k]
+    const float *d_weights;  // [tokens][top_k], gradient only
+    void *d_logits;          // type[tokens], rows d_stride elements apart, gradient only
+    int64_t d_stride;
+};
+
+// Routes in the order of their experts: parts of at least kGroupPart routes, a
+// workgroup each, at most kGroupBlocks of them; one part needs no counts of others.
+constexpr int64_t kGroupMaxExperts = 1024, kGroupPart = 4096, kGroupBlocks = 256;
+constexpr int kGroupWaves = 16;
+constexpr int64_t group_part(int64_t pairs) {
+    const int64_t even = (ceil_of(pairs, kGroupBlocks) + 1023) / 1024 * 1024;
+    return even > kGroupPart ? even : kGroupPart;
+}
+constexpr int64_t group_blocks(int64_t pairs) { return pairs > 0 ? ceil_of(pairs, group_part(pairs)) : 1; }
+constexpr int64_t group_workspace_bytes(int64_t pairs, int64_t experts) {
+    return group_blocks(pairs) > 1 ? 4 * group_blocks(pairs) * experts : 0;
+}
+struct GroupArgs {
+    const int32_t *ids;  // [pairs]
+    int64_t pairs, routes, part;
+    int experts;
+    int32_t *slots, *rows, *offsets, *counts;  // counts: workspace [blocks][experts]
+};
+
+// The operands of the 4-bit products, which are dense, or take routed rows grouped
+// by expert, there plain or gated.
+enum I4Form { kI4Dense, kI4Routed, kI4RoutedGated };
+constexpr int64_t kI4MaxK = 131040, kI4MaxExperts = 1024;
+constexpr int kI4Waves = 4;
+struct I4Product {
+    const int32_t *w;       // [experts][rows][k / 8]
+    const void *w_scale;    // scale type [experts][rows][groups]
+    const int32_t *w_up;    // gated only
+    const void *up_scale;
+    const int32_t *x;       // [x_rows][k / 4]
+    const float *x_scale;   // [x_rows] or NULL (= 1)
+    const float *bias;      // [experts][rows] or NULL, product only
+    const int32_t *index;   // routed: row of x of each routed row, or NULL (the same)
+    const int32_t *offsets; // routed: [experts + 1]
+    int64_t x_rows;
+    int rows, tokens, chunks;      // channels; tokens or routed rows; 32-element chunks of k
+    int groups, chunk_shift;       // groups of a channel, log2 of a group's chunks
+    int experts, act;
+    void *out;
+    int64_t out_stride;
+};
+
 // Kernel launchers.  Arguments are already validated; geometry comes from
 // evaluate_launch.  Each returns the HIP launch status.
 hipError_t launch_copy_f32(const loom_launch_config &cfg, const float *in, float *out, int64_t n,
@@ -646,6 +713,12 @@ hipError_t launch_i8_matmul(const loom_launch_config &cfg, const I8Product &p, i
 
 hipError_t launch_i8_gated_projection(const loom_launch_config &cfg, const I8Product &p, int type,
                                       hipStream_t stream);
+
+hipError_t launch_route_experts(const loom_launch_config &cfg, const RouteArgs &a, hipStream_t stream);
+hipError_t launch_route_experts_backward(const loom_launch_config &cfg, const RouteArgs &a, hipStream_t stream);
+hipError_t launch_group_routes(const loom_launch_config &cfg, const GroupArgs &a, hipStream_t stream);
+hipError_t launch_i4_product(const loom_launch_config &cfg, const I4Product &p, I4Form form, int scale_type, int type,
+                             hipStream_t stream);
 
 // One function a type of d_out and d_x; d_stride: of d_out; d_x, d_gate and d_up may each be NULL
 // (not wanted).

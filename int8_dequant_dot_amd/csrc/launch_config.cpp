@@ -186,6 +186,42 @@ int geo_i8_backward(const int64_t *w, loom_launch_config *c) {
     return geo_i8_tiles(w, true, false, c);
 }
 
+// route_experts, route_experts_backward (tokens, experts, groups, top_k): one
+// workgroup per kRouteWaves waves of tokens, each taking every grid.x-th run once
+// the grid reaches the work-item limit (LDS: the choices of its tokens and the
+// groups' values, where there are groups).
+template <bool BACKWARD>
+int geo_route(const int64_t *w, loom_launch_config *c) {
+    if (w[0] < 0 || w[1] < 1 || w[1] > kRouteMaxExperts || w[2] < 1 || w[2] > kRouteMaxGroups || w[3] < 1 ||
+        w[3] > kRouteMaxTopK)
+        return LOOM_ERR_RANGE;
+    const int64_t size = kRouteWaves * kSubgroupSize, per = size >> route_log_lanes(w[0], w[1], w[3]);
+    return set(c, grid_stride_groups(ceil_div(w[0], per), size), (uint32_t)size,
+               !BACKWARD && w[2] > 1 ? (uint32_t)(8 * per * (w[1] + w[2])) : 0);
+}
+
+// group_routes(pairs, experts): one workgroup per part of group_part routes (LDS:
+// its waves' counts), at least one.
+int geo_group_routes(const int64_t *w, loom_launch_config *c) {
+    if (w[0] < 0 || w[1] < 1 || w[1] > kGroupMaxExperts) return LOOM_ERR_RANGE;
+    return set(c, group_blocks(w[0]), kGroupWaves * kSubgroupSize,
+               (uint32_t)(4 * ((kGroupWaves + 2) * (kGroupMaxExperts + 1) + kGroupWaves)));
+}
+
+// i4_matmul (rows, k, tokens, group), i4_expert_matmul and
+// i4_expert_gated_projection (rows, k, pairs, group, experts): one workgroup per
+// 32 tokens of one expert (at most: routed tiles that the offsets leave empty end
+// at once) and 32 channels a wave.
+template <bool ROUTED>
+int geo_i4(const int64_t *w, loom_launch_config *c) {
+    if (w[0] < 0 || w[1] < 0 || w[1] > kI4MaxK || w[2] < 0 || w[3] < 32) return LOOM_ERR_RANGE;
+    if (ROUTED && (w[4] < 1 || w[4] > kI4MaxExperts)) return LOOM_ERR_RANGE;
+    const int64_t tiles = ROUTED ? w[2] / 32 + (w[2] < w[4] ? w[2] : w[4]) : ceil_div(w[2], 32);
+    const int64_t blocks = ceil_div(w[0], 32 * kI4Waves);
+    if (blocks > 0 && tiles > kMaxGridWorkItems / blocks) return LOOM_ERR_RANGE;
+    return set(c, tiles * blocks, kI4Waves * kSubgroupSize, 0);
+}
+
 struct Export {
     const char *name;
     size_t arity;
@@ -205,6 +241,12 @@ const Export kExports[kExportCount] = {
     {"i8_matmul", 3, geo_i8_product<false>},
     {"i8_gated_projection", 3, geo_i8_product<true>},
     {"i8_gated_projection_backward", 3, geo_i8_backward},
+    {"route_experts", 4, geo_route<false>},
+    {"route_experts_backward", 4, geo_route<true>},
+    {"group_routes", 2, geo_group_routes},
+    {"i4_matmul", 4, geo_i4<false>},
+    {"i4_expert_matmul", 5, geo_i4<true>},
+    {"i4_expert_gated_projection", 5, geo_i4<true>},
 };
 
 }  // namespace
@@ -231,7 +273,7 @@ extern "C" int loom_launch_config_invoke(uint32_t token, const uint64_t *workloa
     if (token == 0 || token > loom::kExportCount) return LOOM_ERR_TOKEN;
     const loom::Export &e = loom::kExports[token - 1];
     if (workload_count != e.arity) return LOOM_ERR_TOKEN;
-    int64_t w[4];
+    int64_t w[8];
     for (size_t i = 0; i < workload_count; ++i) memcpy(&w[i], &workload_bits[i], sizeof(int64_t));
     loom_launch_config tmp;
     const int st = e.geometry(w, &tmp);
