@@ -6,7 +6,7 @@
 //     product: out[t][n] = y[t][n] + bias[n],   gated: act(y_gate) * y_up
 //
 // A group's sum is exact in int32; the groups are added in f32.
-#include "i4_common.hpp"
+#include "i4_tiles.hpp"
 
 namespace loom {
 
@@ -76,24 +76,69 @@ __global__ __launch_bounds__(kI4Waves * kWave) void i4_block_kernel(I4Product p,
     }
 }
 
-template <bool ROUTED, bool GATED>
-hipError_t run(const loom_launch_config &cfg, const I4Product &p, int scale_type, int type, hipStream_t stream) {
+template <bool ROUTED, typename C, int ST>
+__global__ __launch_bounds__(C::NW * kWave, 1) void i4_tile_kernel(I4Product p, int type) {
+    __shared__ __align__(1024) char lds[C::kLds];
+    const uint32_t ch_tiles = count_of(p.rows, C::OUT_CH);
+    I4TileLoop<C, ST> loop{p, lds};
+    loop.lane = lane_id(), loop.half = loop.lane >> 5, loop.m = loop.lane & 31;
+    loop.wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    loop.wm = loop.wave % C::WM, loop.wn = loop.wave / C::WM;
+    loop.expert = 0;
+    uint32_t ch, tok;
+    if constexpr (ROUTED) {
+        tile_of(blockIdx.x, ch_tiles, gridDim.x / ch_tiles, 1, ch, tok);
+        if (!routed_tile<C::TK>(p, tok, loop.expert, loop.t0, loop.rows)) return;
+    } else {
+        tile_of(blockIdx.x, ch_tiles, count_of(p.tokens, C::TK), 8, ch, tok);
+        loop.t0 = (int64_t)tok * C::TK;
+        loop.rows = (int)min((int64_t)C::TK, p.tokens - loop.t0);
+    }
+    loop.n0 = (int64_t)ch * C::OUT_CH;
+    loop.run([&](int r) {
+        int64_t row = loop.t0 + r;
+        if constexpr (ROUTED) x_row(p, loop.t0 + r, row);
+        return row;
+    });
+    loop.store(type, [&](int r) {
+        int64_t row = loop.t0 + r;
+        float scale = 1.0f;
+        if constexpr (ROUTED)
+            if (!x_row(p, loop.t0 + r, row)) scale = __builtin_nanf("");
+        return p.x_scale ? scale * p.x_scale[row] : scale;
+    });
+}
+
+template <bool ROUTED, bool GATED, int ST>
+hipError_t run(const loom_launch_config &cfg, const I4Product &p, int type, hipStream_t stream) {
     const dim3 grid(cfg.workgroups[0]), block(cfg.workgroup_size[0]);
-    switch (scale_type) {
-        case LOOM_F32: hipLaunchKernelGGL((i4_block_kernel<ROUTED, GATED, LOOM_F32>), grid, block, 0, stream, p, type); break;
-        case LOOM_F16: hipLaunchKernelGGL((i4_block_kernel<ROUTED, GATED, LOOM_F16>), grid, block, 0, stream, p, type); break;
-        default: hipLaunchKernelGGL((i4_block_kernel<ROUTED, GATED, LOOM_BF16>), grid, block, 0, stream, p, type);
+    const int subs = i4_subs(p.chunk_shift);
+    if (i4_use_tiles(p.tokens, ROUTED ? p.experts : 0)) {
+        if (subs == 1) hipLaunchKernelGGL((i4_tile_kernel<ROUTED, I4Tile<2, 2, 1, GATED>, ST>), grid, block, 0, stream, p, type);
+        else if (subs == 2) hipLaunchKernelGGL((i4_tile_kernel<ROUTED, I4Tile<2, 2, 2, GATED>, ST>), grid, block, 0, stream, p, type);
+        else hipLaunchKernelGGL((i4_tile_kernel<ROUTED, I4Tile<2, 2, 4, GATED>, ST>), grid, block, 0, stream, p, type);
+    } else {
+        hipLaunchKernelGGL((i4_block_kernel<ROUTED, GATED, ST>), grid, block, 0, stream, p, type);
     }
     return hipGetLastError();
+}
+
+template <bool ROUTED, bool GATED>
+hipError_t run_typed(const loom_launch_config &cfg, const I4Product &p, int scale_type, int type, hipStream_t stream) {
+    switch (scale_type) {
+        case LOOM_F32: return run<ROUTED, GATED, LOOM_F32>(cfg, p, type, stream);
+        case LOOM_F16: return run<ROUTED, GATED, LOOM_F16>(cfg, p, type, stream);
+        default: return run<ROUTED, GATED, LOOM_BF16>(cfg, p, type, stream);
+    }
 }
 
 }  // namespace
 
 hipError_t launch_i4_product(const loom_launch_config &cfg, const I4Product &p, I4Form form, int scale_type, int type,
                              hipStream_t stream) {
-    if (form == kI4Dense) return run<false, false>(cfg, p, scale_type, type, stream);
-    if (form == kI4Routed) return run<true, false>(cfg, p, scale_type, type, stream);
-    return run<true, true>(cfg, p, scale_type, type, stream);
+    if (form == kI4Dense) return run_typed<false, false>(cfg, p, scale_type, type, stream);
+    if (form == kI4Routed) return run_typed<true, false>(cfg, p, scale_type, type, stream);
+    return run_typed<true, true>(cfg, p, scale_type, type, stream);
 }
 
 }  // namespace loom

@@ -1,0 +1,279 @@
+// i4_tiles.hpp -- the tile of the 4-bit products: activations through LDS,
+// weights straight into registers, group sums on the int8 matrix cores.
+#pragma once
+
+#include "i4_common.hpp"
+#include "i8_tiles.hpp"
+
+namespace loom {
+
+// global_load_dwordx4 ... lds: lane l's 16 bytes at its address land at LDS byte
+// at + 16 l.  Not counted by the compiler, as load_to_lds.
+__device__ __forceinline__ void gather_to_lds(const void *from, int at) {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %1, off"
+        :
+        : "s"(at), "v"(from)
+        : "memory", "m0");
+}
+
+// A workgroup computes 32 XT WN tokens x 256 channels with WN x 4 waves, each
+// wave 64 channels (gated: 32 of each projection) as XT x 2 blocks of 32 x 32.
+// A operand: 32 tokens, B: 32 channels; lane l holds 16 elements of token or channel
+// l & 31, half h = l >> 5 of the product's 32, and of the sums channel l & 31, tokens
+// 8 (r >> 2) + 4 h + (r & 3).
+//
+// A step is 256 elements of k, two halves of SUBS groups of 128 / SUBS (with one,
+// part of a longer group).  Product i of a half's four takes the 16-element pieces
+// piece(i, 0) and piece(i, 1): both halves of 32 neighbours where SUBS is 4, else a
+// half each of two 32s, whose weights are then one read for both.
+//
+// LDS holds two steps: rows of 256 bytes of activations and of 128 bytes of
+// weights, filled by direct loads of whole lines; 16-byte piece c of row r sits at
+// slot c ^ (r & 15) or c ^ (r & 7), so that fragment reads meet no bank twice.
+template <int XT_, int WN_, int SUBS_, bool GATED_>
+struct I4Tile {
+    static constexpr int XT = XT_, WN = WN_, SUBS = SUBS_;
+    static constexpr bool GATED = GATED_;
+    static constexpr int WM = 4, NW = WM * WN, WT = 2, TK = 32 * XT * WN, CH = 64 * WM, OUT_CH = GATED ? CH / 2 : CH;
+    static constexpr int kBytesX = TK * 256, kBytesW = CH * 128, kStep = kBytesX + kBytesW;
+    static constexpr int kBytesS = 2 * SUBS * CH * 4;  // a step's scales, as f32
+    static constexpr int kLds = 2 * (kStep + kBytesS);
+    static constexpr int XJ = TK / 4 / NW, WJ = CH / 8 / NW;  // direct loads a wave and step
+    static constexpr int PER = 4 / SUBS;                      // products of a group within a half
+    static_assert(NW * kWave == 2 * CH, "a thread loads the scales of a channel and half");
+    static_assert(TK % (4 * NW) == 0 && CH % (8 * NW) == 0 && kLds <= 160 * 1024, "whole loads a wave");
+    static __device__ constexpr int piece(int i, int h) { return SUBS == 4 ? 2 * i + h : 4 * (i >> 1) + 2 * h + (i & 1); }
+};
+
+template <typename C, int ST>
+struct I4TileLoop {
+    const I4Product &p;
+    char *lds;
+    int lane, wave, wm, wn, half, m;
+    int64_t t0, n0;    // first token (routed row), first output channel of the workgroup
+    int rows, expert;  // rows of the tile
+
+    float acc[C::XT][C::WT][16];
+
+    // LDS weight row r -> its matrix (gated: 32 gate rows and the same 32 up rows a
+    // wave) and its row there.
+    __device__ __forceinline__ bool is_up(int r) const { return C::GATED && (r & 32); }
+    __device__ __forceinline__ int64_t weight_row(int r) const {
+        const int64_t n = n0 + (C::GATED ? (r >> 6) * 32 + (r & 31) : r);
+        return (int64_t)expert * p.rows + min(n, (int64_t)p.rows - 1);
+    }
+    __device__ __forceinline__ const int32_t *matrix(bool up) const { return up ? p.w_up : p.w; }
+    __device__ __forceinline__ const void *scales(bool up) const { return up ? p.up_scale : p.w_scale; }
+
+    // row_of(r): the row of x for row r of the tile.
+    template <typename RowOf>
+    __device__ __forceinline__ void run(RowOf &&row_of) {
+#pragma unroll
+        for (int x = 0; x < C::XT; ++x)
+#pragma unroll
+            for (int w = 0; w < C::WT; ++w)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[x][w][r] = 0.0f;
+        const int steps = p.chunks / 8;
+        const int64_t kb = (int64_t)p.chunks * 32;
+        const char *from_x[C::XJ], *from_w[C::WJ];
+#pragma unroll
+        for (int j = 0; j < C::XJ; ++j) {
+            const int r = (wave + C::NW * j) * 4 + (lane >> 4);
+            from_x[j] = (const char *)p.x + row_of(min(r, rows - 1)) * kb + (((lane & 15) ^ (r & 15)) << 4);
+        }
+#pragma unroll
+        for (int j = 0; j < C::WJ; ++j) {
+            const int r = (wave + C::NW * j) * 8 + (lane >> 3);
+            from_w[j] = (const char *)matrix(is_up(r)) + weight_row(r) * (kb / 2) + (((lane & 7) ^ (r & 7)) << 4);
+        }
+        const int at = lds_address(lds) + wave * 1024;
+        // load J of step s, into that place
+        auto load = [&](auto at_j, int64_t s, int place) {
+            constexpr int j = decltype(at_j)::value, k = j < C::XJ ? 0 : j - C::XJ;
+            const int to = at + (place & 1) * C::kStep;
+            if constexpr (j < C::XJ) gather_to_lds(from_x[j] + s * 256, to + C::NW * j * 1024);
+            else gather_to_lds(from_w[k] + s * 128, to + C::kBytesX + C::NW * k * 1024);
+        };
+        // Scales: read by every wave that uses them, a line for each lane and two bytes, they
+        // took 200 of 1200 us at 4096 x 8192 x 28672.  Each thread reads those of one channel
+        // and half of a step, and they wait in LDS.
+        typedef typename ElementOf<ST>::type Scale;
+        typedef Scale Scales __attribute__((ext_vector_type(C::SUBS), aligned(sizeof(Scale))));
+        const int ch = threadIdx.x >> 1, my_half = threadIdx.x & 1;
+        const Scale *my_scales = (const Scale *)scales(is_up(ch)) + weight_row(ch) * p.groups;
+        float *const held = (float *)(lds + 2 * C::kStep);
+        Scales coming;
+        auto fetch_scales = [&](int s) {
+            s = min(s, steps - 1);
+            coming = *(const Scales *)(my_scales + (C::SUBS > 1 ? (2 * s + my_half) * C::SUBS : (8 * s + 4 * my_half) >> p.chunk_shift));
+        };
+        auto keep_scales = [&](int s) {
+            float *to = held + ((s & 1) * 2 + my_half) * (C::SUBS * C::CH) + ch;
+#pragma unroll
+            for (int u = 0; u < C::SUBS; ++u) to[u * C::CH] = (float)coming[u];
+        };
+        if (steps > 0) {
+            float scale[C::WT][C::SUBS];
+            fetch_scales(0);
+            keep_scales(0);
+            each_index<C::XJ + C::WJ>([&](auto j) { load(j, 0, 0); });
+            each_index<C::XJ + C::WJ>([&](auto j) { load(j, min(1, steps - 1), 1); });
+            wait_loads<C::XJ + C::WJ>();
+            wait_lds();
+            barrier();
+            constexpr int WL = C::SUBS == 4 ? 4 : 2;
+            int4v a[4], raw[C::WT][WL], b[C::WT][4];
+            const char *base_x = lds + (wn * C::XT * 32 + m) * 256, *base_w = lds + C::kBytesX + (wm * 64 + m) * 128;
+            // fragments of half h (0, 1) of the step at that place
+            auto read_a = [&](int place, int h, int x, int i) {
+                a[i] = *(const int4v *)(base_x + place + x * 8192 + (((8 * h + C::piece(i, half)) ^ (m & 15)) << 4));
+            };
+            auto read_w = [&](int place, int h) {
+#pragma unroll
+                for (int w = 0; w < C::WT; ++w)
+#pragma unroll
+                    for (int i = 0; i < WL; ++i) {
+                        const int c = 4 * h + (C::SUBS == 4 ? i : 2 * i + half);
+                        raw[w][i] = *(const int4v *)(base_w + place + w * 4096 + ((c ^ (m & 7)) << 4));
+                    }
+            };
+            auto unpack = [&](int w, int i) {
+                if constexpr (C::SUBS == 4) b[w][i] = half ? i4_high(raw[w][i]) : i4_low(raw[w][i]);
+                else b[w][i] = i & 1 ? i4_high(raw[w][i >> 1]) : i4_low(raw[w][i >> 1]);
+            };
+            read_w(0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                read_a(0, 0, 0, i);
+#pragma unroll
+                for (int w = 0; w < C::WT; ++w) unpack(w, i);
+            }
+            pin();
+            int16v sum[2];
+            for (int s = 0; s < steps; ++s) {
+                const int place = (s & 1) * C::kStep, other = C::kStep - place;
+                const int64_t after = min(s + 2, steps - 1);  // past the end the last step again
+                fetch_scales(s + 1);
+                const float *my = held + (s & 1) * (2 * C::SUBS * C::CH) + wm * 64 + m;
+                // units of PER products that end a group's part, block by block; while one is
+                // multiplied the sums of the one before are converted, scaled and added, and in
+                // the last blocks the next half's fragments are read and unpacked into the
+                // registers that the products leave
+                constexpr int UNITS = C::XT * C::WT * C::SUBS;
+                each_index<2>([&](auto at_h) {
+                    constexpr int h = decltype(at_h)::value;
+                    const int then = h == 0 ? place : other;
+#pragma unroll
+                    for (int w = 0; w < C::WT; ++w)
+#pragma unroll
+                        for (int u = 0; u < C::SUBS; ++u) scale[w][u] = my[(h * C::SUBS + u) * C::CH + w * 32];
+                    each_index<UNITS + 1>([&](auto at_u) {
+                        constexpr int u = decltype(at_u)::value, sub = u % C::SUBS, w = u / C::SUBS % C::WT,
+                                      x = u / C::SUBS / C::WT;
+                        each_index<C::PER>([&](auto at_i) {
+                            constexpr int i = decltype(at_i)::value, q = sub * C::PER + i;
+                            if constexpr (x == C::XT - 1 && w == 0 && q == 0) {
+                                if constexpr (h == 1) {
+                                    // all fragments of this step are in registers, and this wave's part
+                                    // of the next step is in LDS: once every wave is here the next step
+                                    // may be read and this one's place filled
+                                    keep_scales(s + 1);
+                                    wait_loads<0>();
+                                    wait_lds();
+                                    barrier();
+                                }
+                                read_w(then, 1 - h);
+                            }
+                            if constexpr (u < UNITS)
+                                sum[u & 1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[q], b[w][q], i == 0 ? int16v{} : sum[u & 1], 0, 0, 0);
+                            if constexpr (u < UNITS && w == C::WT - 1) {
+                                if constexpr (x + 1 < C::XT) read_a(place, h, x + 1, q);
+                                else read_a(then, 1 - h, 0, q);
+                            }
+                            if constexpr (u < UNITS && x == C::XT - 1 && w == C::WT - 1) {
+#pragma unroll
+                                for (int y = 0; y < C::WT; ++y) unpack(y, q);
+                            }
+                            if constexpr (h == 1 && u < UNITS && x == C::XT - 1) {
+                                constexpr int n = w * 4 + q, J = C::XJ + C::WJ;
+                                each_index<J>([&](auto at_j) {
+                                    if constexpr (decltype(at_j)::value * 4 * C::WT / J == n) load(at_j, after, s);
+                                });
+                            }
+                            if constexpr (u > 0) {
+                                constexpr int v = u - 1, vs = v % C::SUBS, vw = v / C::SUBS % C::WT, vx = v / C::SUBS / C::WT;
+#pragma unroll
+                                for (int r = i * 16 / C::PER; r < (i + 1) * 16 / C::PER; ++r)
+                                    acc[vx][vw][r] = __builtin_fmaf((float)sum[v & 1][r], scale[vw][vs], acc[vx][vw][r]);
+                            }
+                            pin();
+                        });
+                    });
+                });
+            }
+            wait_loads<0>();
+        }
+        // the rest of k, up to seven times 32 elements, in parts of a group and at most 128
+        constexpr int kPart = 4 / C::SUBS;
+        for (int c0 = 8 * steps; c0 < p.chunks; c0 += kPart) {
+            const int c1 = min(c0 + kPart, p.chunks), g = c0 >> p.chunk_shift;
+#pragma unroll
+            for (int x = 0; x < C::XT; ++x) {
+                const int4v *xr = (const int4v *)((const char *)p.x + row_of(min((wn * C::XT + x) * 32 + m, rows - 1)) * kb);
+                int16v sum[C::WT] = {};
+                for (int c = c0; c < c1; ++c)
+#pragma unroll
+                    for (int w = 0; w < C::WT; ++w) {
+                        const int64_t row = weight_row(wm * 64 + w * 32 + m);
+                        const int4v v = ((const int4v *)matrix(C::GATED && w))[row * p.chunks + c];
+                        sum[w] = __builtin_amdgcn_mfma_i32_32x32x32_i8(xr[2 * c + half], half ? i4_high(v) : i4_low(v), sum[w], 0, 0, 0);
+                    }
+#pragma unroll
+                for (int w = 0; w < C::WT; ++w) {
+                    const float scale = scale_at<ST>(scales(C::GATED && w), weight_row(wm * 64 + w * 32 + m) * p.groups + g);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[x][w][r] = __builtin_fmaf((float)sum[w][r], scale, acc[x][w][r]);
+                }
+            }
+        }
+    }
+
+    // scale_of(r): x_scale of row r of the tile.
+    template <typename ScaleOf>
+    __device__ __forceinline__ void store(int type, ScaleOf &&scale_of) {
+#pragma unroll
+        for (int x = 0; x < C::XT; ++x) {
+            const int first = (wn * C::XT + x) * 32;
+            if (first >= rows) return;
+            const float xs = scale_of(min(first + m, rows - 1));
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = 8 * (r >> 2) + 4 * half + (r & 3);
+                const float scale = __shfl(xs, row);
+                const int64_t out = (t0 + first + row) * p.out_stride;
+                const bool live = first + row < rows;
+                if constexpr (C::GATED) {
+                    const int64_t n = n0 + wm * 32 + m;
+                    const float y = act_value(p.act, acc[x][0][r] * kI4Unit * scale) * (acc[x][1][r] * kI4Unit * scale);
+                    if (live && n < p.rows) store1(p.out, type, out + n, y);
+                } else {
+#pragma unroll
+                    for (int w = 0; w < C::WT; ++w) {
+                        const int64_t n = n0 + wm * 64 + w * 32 + m;
+                        float y = acc[x][w][r] * kI4Unit * scale;
+                        if (live && n < p.rows) {
+                            if (p.bias) y = y + p.bias[(int64_t)expert * p.rows + n];
+                            store1(p.out, type, out + n, y);
+                        }
+                    }
+                }
+            }
+        }
+    }
+};
+
+}  // namespace loom

@@ -656,6 +656,8 @@ struct GroupArgs {
 enum I4Form { kI4Dense, kI4Routed, kI4RoutedGated };
 constexpr int64_t kI4MaxK = 131040, kI4MaxExperts = 1024;
 constexpr int kI4Waves = 4;
+constexpr int i4_subs(int chunk_shift) { return chunk_shift >= 2 ? 1 : chunk_shift == 1 ? 2 : 4; }
+constexpr bool i4_use_tiles(int64_t tokens, int64_t experts) { return tokens > (experts > 0 ? 32 * experts : 32); }
 struct I4Product {
     const int32_t *w;       // [experts][rows][k / 8]
     const void *w_scale;    // scale type [experts][rows][groups]

@@ -212,14 +212,16 @@ int geo_group_routes(const int64_t *w, loom_launch_config *c) {
 // i4_expert_gated_projection (rows, k, pairs, group, experts): one workgroup per
 // 32 tokens of one expert (at most: routed tiles that the offsets leave empty end
 // at once) and 32 channels a wave.
-template <bool ROUTED>
+template <bool ROUTED, bool GATED>
 int geo_i4(const int64_t *w, loom_launch_config *c) {
     if (w[0] < 0 || w[1] < 0 || w[1] > kI4MaxK || w[2] < 0 || w[3] < 32) return LOOM_ERR_RANGE;
     if (ROUTED && (w[4] < 1 || w[4] > kI4MaxExperts)) return LOOM_ERR_RANGE;
-    const int64_t tiles = ROUTED ? w[2] / 32 + (w[2] < w[4] ? w[2] : w[4]) : ceil_div(w[2], 32);
-    const int64_t blocks = ceil_div(w[0], 32 * kI4Waves);
+    const bool big = i4_use_tiles(w[2], ROUTED ? w[4] : 0);
+    const int64_t tokens = big ? 128 : 32, channels = big ? (GATED ? 128 : 256) : 32 * kI4Waves;
+    const int64_t tiles = ROUTED ? w[2] / tokens + (w[2] < w[4] ? w[2] : w[4]) : ceil_div(w[2], tokens);
+    const int64_t blocks = ceil_div(w[0], channels);
     if (blocks > 0 && tiles > kMaxGridWorkItems / blocks) return LOOM_ERR_RANGE;
-    return set(c, tiles * blocks, kI4Waves * kSubgroupSize, 0);
+    return set(c, tiles * blocks, (big ? 8 : kI4Waves) * kSubgroupSize, big ? 160 * 1024 : 0);
 }
 
 struct Export {
@@ -244,9 +246,9 @@ const Export kExports[kExportCount] = {
     {"route_experts", 4, geo_route<false>},
     {"route_experts_backward", 4, geo_route<true>},
     {"group_routes", 2, geo_group_routes},
-    {"i4_matmul", 4, geo_i4<false>},
-    {"i4_expert_matmul", 5, geo_i4<true>},
-    {"i4_expert_gated_projection", 5, geo_i4<true>},
+    {"i4_matmul", 4, geo_i4<false, false>},
+    {"i4_expert_matmul", 5, geo_i4<true, false>},
+    {"i4_expert_gated_projection", 5, geo_i4<true, true>},
 };
 
 }  // namespace

@@ -8,9 +8,9 @@ largest, which is what the rounding of the exponent l - max costs, in units of u
    at most 64 of them (at most 6 additions deep): 2 d + 32.
  - gradients are products of these with differences whose parts are bounded by the sums of magnitudes: 2 d + 64 (4 d + 64
    renormalised) times those sums.
- - a group's sum in the 4-bit product is exact in int32, its conversion is within u, and each of the n additions rounds a
-   partial sum that is at most the sum of magnitudes: (n + 8) u times that sum, n the groups, then one u for x_scale and
-   one for the bias.
+ - the 4-bit product adds groups, and parts of 128 of longer groups, whose sums are exact in int32: a part's conversion is
+   within u, and each of the n additions rounds a partial sum that is at most the sum of the parts' magnitudes: (n + 8) u
+   times that sum, n the parts, then one u for x_scale and one for the bias.
 """
 import math
 
@@ -370,19 +370,24 @@ def operands(experts, rows, k, x_rows, group, scales, seed, names=("w",)):
 
 
 def product64(x, w, ws, group):
-    """-> (sum over groups of scale * sum, the same sum of magnitudes)."""
+    """-> (sum over groups of scale * sum, the same sum of magnitudes of groups and parts of 128 of longer ones)."""
     y = torch.zeros(x.shape[0], w.shape[0], dtype=torch.float64)
     size = y.clone()
-    for g in range(ws.shape[1]):
-        part = slice(g * group, (g + 1) * group)
-        term = (x[:, part].double() @ w[:, part].double().t()) * ws[:, g].double()
+    step = min(group, 128)
+    for at in range(0, x.shape[1], step):
+        part = slice(at, at + step)
+        term = (x[:, part].double() @ w[:, part].double().t()) * ws[:, at // group].double()
         y += term
         size += term.abs()
     return y, size
 
 
+def parts(k, group):
+    return -(-k // min(group, 128))
+
+
 def bounded(y, size, groups, xs, bias, dtype):
-    """-> (the value, its tolerance)."""
+    """-> (the value, its tolerance); groups: how many parts are added."""
     v, s = (y, size) if xs is None else (y * xs.double()[:, None], size * xs.double()[:, None].abs())
     tol = (groups + 10) * U * s
     if bias is not None:
@@ -409,7 +414,7 @@ def test_i4_matmul(loom, device, rows, k, tokens, group):
         s = operands(1, rows, k, tokens, group, scales, rows + k + tokens)
         d = {n: t.to(device) for n, t in s.items()}
         y, size = product64(s["x"], s["w"][0], s["ws"][0], group)
-        n = s["ws"].shape[2]
+        n = parts(k, group)
         w, x = loom.pack_int4(d["w"][0]), loom.pack_int8(d["x"])
         got = loom.i4_matmul(w, d["ws"][0], x, d["xs"], bias=d["bias"][0], group=group, dtype=dtype)
         assert got.dtype == dtype and tuple(got.shape) == (tokens, rows)
@@ -449,7 +454,7 @@ def test_i4_matmul_views_and_scales(loom, device):
         s = operands(1, rows, k, tokens, group, F32, 5)
         d = {n: t.to(device) for n, t in s.items()}
         y, size = product64(s["x"], s["w"][0], s["ws"][0], group)
-        n = s["ws"].shape[2]
+        n = parts(k, group)
         w, x = loom.pack_int4(d["w"][0]), loom.pack_int8(d["x"])
         wb = torch.full((rows * k // 8 + 8,), -1, dtype=torch.int32, device=device)
         xb = torch.full((tokens * k // 4 + 8,), -1, dtype=torch.int32, device=device)
@@ -469,7 +474,7 @@ def test_i4_matmul_views_and_scales(loom, device):
         check(got[3:], *(t[3:] for t in bounded(y, size, n, xs.nan_to_num(0, 0, 0), None, F32)))
         # a NaN scale of a group reaches its channel and no other
         ws = s["ws"][0].clone()
-        ws[rows // 2, n - 1] = NAN
+        ws[rows // 2, -1] = NAN
         got = loom.i4_matmul(w, ws.to(device), x, group=group, dtype=F32).cpu()
         assert bool(got[:, rows // 2].isnan().all()) and int(got.isnan().sum()) == tokens
     one = loom.i4_matmul(w, d["ws"][0], x[0], group=group, dtype=F32)
@@ -505,7 +510,7 @@ def test_experts(loom, device, counts, rows, k, group):
     g = torch.Generator().manual_seed(rows + k)
     for dtype, scales, act in ((F32, F16, "silu"), (BF16, F32, "gelu"), (F16, BF16, "relu"), (F32, F32, "gelu_tanh")):
         s = operands(experts, rows, k, pairs, group, scales, rows * 3 + k, ("w", "u"))
-        n = s["ws"].shape[2]
+        n = parts(k, group)
         d = {m: t.to(device) for m, t in s.items()}
         w, u, x = loom.pack_int4(d["w"]), loom.pack_int4(d["u"]), loom.pack_int8(d["x"])
         index = torch.randint(0, pairs, (pairs,), generator=g, dtype=torch.int32) if act in ("silu", "relu") else None
