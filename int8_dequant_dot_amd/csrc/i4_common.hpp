@@ -23,12 +23,22 @@ __device__ __forceinline__ float scale_at(const void *scales, int64_t at) {
     return (float)((const typename ElementOf<ST>::type *)scales)[at];
 }
 
-// Tile `index` of the routes grouped by expert, in tiles of up to TOKENS rows of
+// Sums over the lanes up to and including this one.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr:1, 2, 4, 8 within 16 lanes
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+    return v;
+}
+
+// Tile `index` of the routes grouped by expert, in tiles of up to `size` rows of
 // one expert: which expert, its first row and how many.  Every lane takes part
 // and returns the same; false past the last tile.  offsets that are out of order
 // or out of range make an expert's rows fewer, never others.
-template <int TOKENS>
-__device__ __forceinline__ bool routed_tile(const I4Product &p, int64_t index, int &expert, int64_t &first, int &rows) {
+__device__ __forceinline__ bool routed_tile(const I4Product &p, int size, int64_t index, int &expert, int64_t &first, int &rows) {
     const int lane = lane_id();
     int64_t before = 0;
     for (int e0 = 0; e0 < p.experts; e0 += kWave) {
@@ -38,19 +48,15 @@ __device__ __forceinline__ bool routed_tile(const I4Product &p, int64_t index, i
             begin = max(p.offsets[e], 0);
             end = min(p.offsets[e + 1], p.tokens);
         }
-        const int n = end > begin ? end - begin : 0, tiles = (n + TOKENS - 1) / TOKENS;
-        int scan = tiles;
-        for (int d = 1; d < kWave; d *= 2) {
-            const int v = __shfl_up(scan, d);
-            if (lane >= d) scan += v;
-        }
+        const int n = end > begin ? end - begin : 0, tiles = (int)(((int64_t)n + size - 1) / size);
+        const int scan = wave_scan(tiles);
         const uint64_t past = __ballot(before + scan > index);
         if (past) {
             const int at = __builtin_ctzll(past);
             const int skip = (int)(index - before) - (readlane(scan, at) - readlane(tiles, at));
             expert = e0 + at;
-            first = (int64_t)readlane(begin, at) + (int64_t)skip * TOKENS;
-            rows = min(readlane(n, at) - skip * TOKENS, TOKENS);
+            first = (int64_t)readlane(begin, at) + (int64_t)skip * size;
+            rows = min(readlane(n, at) - skip * size, size);
             return true;
         }
         before += readlane(scan, kWave - 1);

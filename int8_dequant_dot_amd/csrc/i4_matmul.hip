@@ -12,114 +12,256 @@ namespace loom {
 
 namespace {
 
-// One wave a block of 32 tokens x 32 channels (gated: of both projections).
-// A operand: 32 tokens, B: 32 channels; lane l holds 16 elements of k, from
-// 16 (l >> 5) on, of token or channel l & 31, and of the sums channel l & 31,
-// tokens 8 (r >> 2) + 4 (l >> 5) + (r & 3).
-template <bool ROUTED, bool GATED, int ST>
-__global__ __launch_bounds__(kI4Waves * kWave) void i4_block_kernel(I4Product p, int type) {
-    const int lane = lane_id(), wave = threadIdx.x / kWave, half = lane >> 5;
-    const int64_t blocks = (p.rows + 32 * kI4Waves - 1) / (32 * kI4Waves);
-    const int64_t tile = blockIdx.x / blocks, n0 = (blockIdx.x % blocks) * (32 * kI4Waves) + wave * 32;
-    int expert = 0, rows;
-    int64_t t0;
+// Few tokens: the weights stream once from memory, straight into the matrix cores'
+// operand registers.  A workgroup owns 32 weight rows (gated: 16 gate rows and the
+// same 16 up rows); its waves each take a contiguous share of k in records of 32 rows
+// x 256 bytes (512 elements), and their partial sums are added in wave order.  One
+// load reads 4 rows x 256 contiguous bytes: lane l holds bytes 64 (l & 3) +
+// 16 (l >> 4) .. + 15 of row 4 i + (l >> 2 & 3), so a product's 16 rows are 4 weight
+// rows x 4 segments of 128 elements, and the 16 columns of B are 4 token slots x the
+// same segments.  Of the sums only those of equal segments are wanted: element
+// e = l & 3 of lane l, row 4 i + (l >> 4), slot 4 v + (l >> 2 & 3); they are scaled and
+// added in f32.
+//
+// A segment of 128 is a group, or a part of one.  Of shorter groups it holds SUB = 2 or
+// 4: a token then takes SUB slots, each of which sees the quarters l >> 4 of its own
+// group and zeros elsewhere.
+template <int ST, int RI, int VG>
+struct I4Record {
+    int4v w[RI], x[VG][2];
+    typename ElementOf<ST>::type scale[RI];
+};
+
+template <bool ROUTED, bool GATED, int ST, int VG>
+__global__ __launch_bounds__(kWave * kI4StreamWaves, 2) void i4_stream_kernel(I4Product p, int type) {
+    constexpr int KS = kI4StreamWaves, RI = kI4StreamLoads, ROWS = 4 * RI, OC = GATED ? ROWS / 2 : ROWS, kSlots = 4 * VG;
+    __shared__ float part[KS][kSlots * ROWS];
+    const int lane = lane_id(), m = lane & 15, quarter = lane >> 4, slot = m >> 2, segment = m & 3;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    const int sub_shift = 2 - min(p.chunk_shift, 2), sub = slot & ((1 << sub_shift) - 1), fit = kSlots >> sub_shift;
+    const uint32_t blocks = count_of(p.rows, OC);
+    int expert = 0, tokens = p.tokens;
+    int64_t t0 = 0;
+    uint32_t block = blockIdx.x;
     if constexpr (ROUTED) {
-        if (!routed_tile<32>(p, tile, expert, t0, rows)) return;
-    } else {
-        t0 = tile * 32;
-        rows = (int)min((int64_t)32, p.tokens - t0);
+        const uint32_t tile = blockIdx.x / blocks;
+        block = blockIdx.x - tile * blocks;
+        if (!routed_tile(p, fit, tile, expert, t0, tokens)) return;
     }
-    if (n0 >= p.rows) return;
-    const int64_t n = min(n0 + (lane & 31), (int64_t)p.rows - 1), t = t0 + min(lane & 31, rows - 1);
-    int64_t xr = t;
-    float xs = 1.0f;
-    if constexpr (ROUTED) {
-        if (!x_row(p, t, xr)) xs = __builtin_nanf("");
+    const int64_t n0 = (int64_t)block * OC, row0 = (int64_t)expert * p.rows + n0;
+    const int left = (int)min((int64_t)OC, p.rows - n0);
+    const int at = 4 * segment + quarter;  // 32-element chunk of the record
+    // offsets from the tile's first rows, whose addresses are the same in every lane
+    typedef typename ElementOf<ST>::type Scale;
+    const int4v *const wbase[2] = {(const int4v *)p.w + row0 * p.chunks, (const int4v *)(GATED ? p.w_up : p.w) + row0 * p.chunks};
+    const Scale *const sbase[2] = {(const Scale *)p.w_scale + row0 * p.groups,
+                                   (const Scale *)(GATED ? p.up_scale : p.w_scale) + row0 * p.groups};
+    const int4v *xrow[VG];
+    uint32_t wrow[RI], srow[RI];
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+        // row 4 i + slot of the operand, 4 i + quarter of the sums
+        wrow[i] = (uint32_t)(min((4 * i + slot) % OC, left - 1) * p.chunks + at);
+        srow[i] = (uint32_t)(min((4 * i + quarter) % OC, left - 1) * p.groups);
     }
-    if (p.x_scale) xs *= p.x_scale[xr];
-    const int64_t wr = (int64_t)expert * p.rows + n;
-    const int4v *x = (const int4v *)p.x + xr * p.chunks * 2 + half;
-    const int4v *w = (const int4v *)p.w + wr * p.chunks, *u = GATED ? (const int4v *)p.w_up + wr * p.chunks : w;
-    float acc[GATED ? 2 : 1][16];
+    bool live[VG];
 #pragma unroll
-    for (int m = 0; m < (GATED ? 2 : 1); ++m)
+    for (int v = 0; v < VG; ++v) {
+        const int token = (4 * v + slot) >> sub_shift;
+        live[v] = token < tokens && quarter >> (2 - sub_shift) == sub;
+        int64_t row = t0 + min(token, tokens - 1);
+        if constexpr (ROUTED) x_row(p, row, row);
+        xrow[v] = (const int4v *)p.x + row * p.chunks * 2 + 2 * at;
+    }
+    float acc[RI][VG];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[m][r] = 0.0f;
-    const int per = 1 << p.chunk_shift;  // 32-element chunks of a group
-    for (int g = 0; g < p.groups; ++g) {
-        int16v sum[2] = {};
-        for (int c = g * per; c < min(g * per + per, p.chunks); ++c) {
-            const int4v a = x[2 * c];
+    for (int i = 0; i < RI; ++i)
 #pragma unroll
-            for (int m = 0; m < (GATED ? 2 : 1); ++m) {
-                const int4v v = m ? u[c] : w[c];
-                sum[m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, half ? i4_high(v) : i4_low(v), sum[m], 0, 0, 0);
+        for (int v = 0; v < VG; ++v) acc[i][v] = 0.0f;
+    auto consume = [&](const I4Record<ST, RI, VG> &q) {
+        int4v b[VG][2];
+#pragma unroll
+        for (int v = 0; v < VG; ++v) {
+            b[v][0] = live[v] ? q.x[v][0] : int4v{};
+            b[v][1] = live[v] ? q.x[v][1] : int4v{};
+        }
+        // two rows of products at a time: more would cost registers, and with them waves
+#pragma unroll
+        for (int i0 = 0; i0 < RI; i0 += 2) {
+            int4v d[2][VG];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int4v low = i4_low(q.w[i0 + i]);
+#pragma unroll
+                for (int v = 0; v < VG; ++v) d[i][v] = __builtin_amdgcn_mfma_i32_16x16x64_i8(low, b[v][0], int4v{}, 0, 0, 0);
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int4v high = i4_high(q.w[i0 + i]);
+#pragma unroll
+                for (int v = 0; v < VG; ++v) d[i][v] = __builtin_amdgcn_mfma_i32_16x16x64_i8(high, b[v][1], d[i][v], 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int v = 0; v < VG; ++v) {
+                    const int4v e = d[i][v];
+                    const int lo = segment & 1 ? e[1] : e[0], hi = segment & 1 ? e[3] : e[2];
+                    acc[i0 + i][v] = __builtin_fmaf((float)(segment & 2 ? hi : lo), (float)q.scale[i0 + i], acc[i0 + i][v]);
+                }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    const int all = p.chunks / 16, per_wave = (all + KS - 1) / KS;
+    const int first = min(all, wave * per_wave), records = min(all, first + per_wave) - first;
+    int c = first * 16;
+    const int group_at = 4 * segment + (sub << (2 - sub_shift));
+    pipelined<2, I4Record<ST, RI, VG>>(
+        records,
+        [&]() {
+            I4Record<ST, RI, VG> q;
+#pragma unroll
+            for (int i = 0; i < RI; ++i) q.w[i] = __builtin_nontemporal_load(wbase[i >= RI / 2] + wrow[i] + (uint32_t)c);
+#pragma unroll
+            for (int i = 0; i < RI; ++i) q.scale[i] = sbase[i >= RI / 2][srow[i] + (uint32_t)((c + group_at) >> p.chunk_shift)];
+#pragma unroll
+            for (int v = 0; v < VG; ++v) q.x[v][0] = xrow[v][2 * c], q.x[v][1] = xrow[v][2 * c + 1];
+            c += 16;
+            return q;
+        },
+        consume);
+    if (p.chunks % 16 && wave == KS - 1) {  // the rest of the row: chunks past it are zero
+        const bool there = all * 16 + at < p.chunks;
+        I4Record<ST, RI, VG> q;
+#pragma unroll
+        for (int i = 0; i < RI; ++i) {
+            q.w[i] = there ? wbase[i >= RI / 2][wrow[i] + (uint32_t)(all * 16)] : int4v{};
+            q.scale[i] = sbase[i >= RI / 2][srow[i] + (uint32_t)min((all * 16 + group_at) >> p.chunk_shift, p.groups - 1)];
         }
 #pragma unroll
-        for (int m = 0; m < (GATED ? 2 : 1); ++m) {
-            const float s = scale_at<ST>(m ? p.up_scale : p.w_scale, wr * p.groups + g);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[m][r] = __builtin_fmaf((float)sum[m][r], s, acc[m][r]);
+        for (int v = 0; v < VG; ++v) {
+            q.x[v][0] = there ? xrow[v][2 * all * 16] : int4v{};
+            q.x[v][1] = there ? xrow[v][2 * all * 16 + 1] : int4v{};
         }
+        consume(q);
     }
-    const bool there = n0 + (lane & 31) < p.rows;
-    const float bias = !GATED && p.bias ? p.bias[wr] : 0.0f;
+    // each quad adds its output's 4 segments; its first lane publishes the sum
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int row = 8 * (r >> 2) + 4 * half + (r & 3);
-        const float scale = __shfl(xs, row);
-        float y = acc[0][r] * kI4Unit * scale;
-        if constexpr (GATED) y = act_value(p.act, y) * (acc[GATED ? 1 : 0][r] * kI4Unit * scale);
-        else if (p.bias) y = y + bias;
-        if (there && row < rows) store1(p.out, type, (t0 + row) * p.out_stride + n, y);
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+        for (int v = 0; v < VG; ++v) {
+            const float t = group_sum<2>(acc[i][v]);
+            if (segment == 0) part[wave][(4 * v + slot) * ROWS + 4 * i + quarter] = t;
+        }
+    __syncthreads();
+    for (int o = threadIdx.x; o < fit * OC; o += kWave * KS) {
+        const int t = o / OC, r = o % OC;
+        if (t >= tokens || r >= left) continue;
+        float sum = 0.0f, up = 0.0f;
+#pragma unroll
+        for (int w = 0; w < KS; ++w)
+            for (int u = 0; u < 1 << sub_shift; ++u) {
+                const float *from = &part[w][((t << sub_shift) + u) * ROWS + r];
+                sum += from[0];
+                if (GATED) up += from[OC];
+            }
+        int64_t row = t0 + t;
+        float xs = 1.0f;
+        if constexpr (ROUTED)
+            if (!x_row(p, row, row)) xs = __builtin_nanf("");
+        if (p.x_scale) xs *= p.x_scale[row];
+        float y = sum * kI4Unit * xs;
+        if (GATED) y = act_value(p.act, y) * (up * kI4Unit * xs);
+        else if (p.bias) y = y + p.bias[row0 + r];
+        store1(p.out, type, (t0 + t) * p.out_stride + n0 + r, y);
     }
 }
 
+// Several split waves (of one wave's tile each) share a tile: each takes a run of k over
+// LDS of its own, with no barrier, and the sums are added in their order at the end.
 template <bool ROUTED, typename C, int ST>
-__global__ __launch_bounds__(C::NW * kWave, 1) void i4_tile_kernel(I4Product p, int type) {
-    __shared__ __align__(1024) char lds[C::kLds];
+__global__ __launch_bounds__(C::kShape.waves() * kWave, 1) void i4_tile_kernel(I4Product p, int type) {
+    constexpr int S = C::kShape.split;
+    static_assert(S == 1 || (C::NW == 1 && C::kLds >= C::XT * C::WT * 4096), "the sums fit the steps");
+    __shared__ __align__(1024) char lds[S * C::kLds];
     const uint32_t ch_tiles = count_of(p.rows, C::OUT_CH);
-    I4TileLoop<C, ST> loop{p, lds};
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    I4TileLoop<C, ST> loop{p, lds + (S > 1 ? wave * C::kLds : 0)};
     loop.lane = lane_id(), loop.half = loop.lane >> 5, loop.m = loop.lane & 31;
-    loop.wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    loop.wave = S > 1 ? 0 : wave;
     loop.wm = loop.wave % C::WM, loop.wn = loop.wave / C::WM;
     loop.expert = 0;
     uint32_t ch, tok;
     if constexpr (ROUTED) {
         tile_of(blockIdx.x, ch_tiles, gridDim.x / ch_tiles, 1, ch, tok);
-        if (!routed_tile<C::TK>(p, tok, loop.expert, loop.t0, loop.rows)) return;
+        if (!routed_tile(p, C::TK, tok, loop.expert, loop.t0, loop.rows)) return;
     } else {
         tile_of(blockIdx.x, ch_tiles, count_of(p.tokens, C::TK), 8, ch, tok);
         loop.t0 = (int64_t)tok * C::TK;
         loop.rows = (int)min((int64_t)C::TK, p.tokens - loop.t0);
     }
     loop.n0 = (int64_t)ch * C::OUT_CH;
-    loop.run([&](int r) {
+    const int all = p.chunks / 8, begin = S > 1 ? (int)((int64_t)all * wave / S) : 0;
+    const int end = S > 1 ? (int)((int64_t)all * (wave + 1) / S) : all;
+    loop.run(begin, end - begin, S == 1 || wave == S - 1, [&](int r) {
         int64_t row = loop.t0 + r;
         if constexpr (ROUTED) x_row(p, loop.t0 + r, row);
         return row;
     });
-    loop.store(type, [&](int r) {
+    auto scale_of = [&](int r) {
         int64_t row = loop.t0 + r;
         float scale = 1.0f;
         if constexpr (ROUTED)
             if (!x_row(p, loop.t0 + r, row)) scale = __builtin_nanf("");
         return p.x_scale ? scale * p.x_scale[row] : scale;
-    });
+    };
+    if constexpr (S > 1) {
+        constexpr int N = 16 / S;  // sums of each block that a wave adds and stores
+#pragma unroll
+        for (int x = 0; x < C::XT; ++x)
+#pragma unroll
+            for (int w = 0; w < C::WT; ++w)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) ((float *)loop.lds)[((x * C::WT + w) * 16 + r) * kWave + loop.lane] = loop.acc[x][w][r];
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < C::XT; ++x)
+#pragma unroll
+            for (int w = 0; w < C::WT; ++w)
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < S; ++q)
+                        sum += ((const float *)(lds + q * C::kLds))[((x * C::WT + w) * 16 + wave * N + e) * kWave + loop.lane];
+                    loop.acc[x][w][e] = sum;
+                }
+        loop.template store<N>(type, wave * N, scale_of);
+    } else {
+        loop.template store<16>(type, 0, scale_of);
+    }
+}
+
+template <bool ROUTED, bool GATED, int ST, int SHAPE = 0>
+void launch_tile(int shape, int subs, dim3 grid, dim3 block, const I4Product &p, int type, hipStream_t stream) {
+    if constexpr (SHAPE < kI4TileCount) {
+        if (shape != SHAPE) return launch_tile<ROUTED, GATED, ST, SHAPE + 1>(shape, subs, grid, block, p, type, stream);
+        if (subs == 1) hipLaunchKernelGGL((i4_tile_kernel<ROUTED, I4Tile<SHAPE, 1, GATED>, ST>), grid, block, 0, stream, p, type);
+        else if (subs == 2) hipLaunchKernelGGL((i4_tile_kernel<ROUTED, I4Tile<SHAPE, 2, GATED>, ST>), grid, block, 0, stream, p, type);
+        else hipLaunchKernelGGL((i4_tile_kernel<ROUTED, I4Tile<SHAPE, 4, GATED>, ST>), grid, block, 0, stream, p, type);
+    }
 }
 
 template <bool ROUTED, bool GATED, int ST>
 hipError_t run(const loom_launch_config &cfg, const I4Product &p, int type, hipStream_t stream) {
     const dim3 grid(cfg.workgroups[0]), block(cfg.workgroup_size[0]);
-    const int subs = i4_subs(p.chunk_shift);
-    if (i4_use_tiles(p.tokens, ROUTED ? p.experts : 0)) {
-        if (subs == 1) hipLaunchKernelGGL((i4_tile_kernel<ROUTED, I4Tile<2, 2, 1, GATED>, ST>), grid, block, 0, stream, p, type);
-        else if (subs == 2) hipLaunchKernelGGL((i4_tile_kernel<ROUTED, I4Tile<2, 2, 2, GATED>, ST>), grid, block, 0, stream, p, type);
-        else hipLaunchKernelGGL((i4_tile_kernel<ROUTED, I4Tile<2, 2, 4, GATED>, ST>), grid, block, 0, stream, p, type);
-    } else {
-        hipLaunchKernelGGL((i4_block_kernel<ROUTED, GATED, ST>), grid, block, 0, stream, p, type);
-    }
+    const int64_t experts = ROUTED ? p.experts : 0;
+    const int subs = i4_subs(p.chunk_shift), slots = i4_stream_slots(p.tokens, experts, subs);
+    if (slots == 4) hipLaunchKernelGGL((i4_stream_kernel<ROUTED, GATED, ST, 1>), grid, block, 0, stream, p, type);
+    else if (slots == 8) hipLaunchKernelGGL((i4_stream_kernel<ROUTED, GATED, ST, 2>), grid, block, 0, stream, p, type);
+    else
+        launch_tile<ROUTED, GATED, ST>(i4_tile_choice(p.rows, 32 * (int64_t)p.chunks, p.tokens, experts, GATED, subs), subs, grid,
+                                       block, p, type, stream);
     return hipGetLastError();
 }
 

@@ -19,8 +19,8 @@ __device__ __forceinline__ void gather_to_lds(const void *from, int at) {
         : "memory", "m0");
 }
 
-// A workgroup computes 32 XT WN tokens x 256 channels with WN x 4 waves, each
-// wave 64 channels (gated: 32 of each projection) as XT x 2 blocks of 32 x 32.
+// A tile is 32 XT WN tokens x 32 WM WT channels (gated: half of them gate, half up rows
+// of the same channels), computed by WN x WM waves, each XT x WT blocks of 32 x 32.
 // A operand: 32 tokens, B: 32 channels; lane l holds 16 elements of token or channel
 // l & 31, half h = l >> 5 of the product's 32, and of the sums channel l & 31, tokens
 // 8 (r >> 2) + 4 h + (r & 3).
@@ -33,18 +33,20 @@ __device__ __forceinline__ void gather_to_lds(const void *from, int at) {
 // LDS holds two steps: rows of 256 bytes of activations and of 128 bytes of
 // weights, filled by direct loads of whole lines; 16-byte piece c of row r sits at
 // slot c ^ (r & 15) or c ^ (r & 7), so that fragment reads meet no bank twice.
-template <int XT_, int WN_, int SUBS_, bool GATED_>
+template <int SHAPE, int SUBS_, bool GATED_>
 struct I4Tile {
-    static constexpr int XT = XT_, WN = WN_, SUBS = SUBS_;
+    static constexpr I4TileShape kShape = i4_tile_shape(SHAPE, GATED_);
+    static constexpr int XT = kShape.xt, WN = kShape.wn, WM = kShape.wm, WT = kShape.wt, SUBS = SUBS_;
     static constexpr bool GATED = GATED_;
-    static constexpr int WM = 4, NW = WM * WN, WT = 2, TK = 32 * XT * WN, CH = 64 * WM, OUT_CH = GATED ? CH / 2 : CH;
+    static constexpr int NW = WM * WN, TK = kShape.tokens(), CH = kShape.channels(), OUT_CH = GATED ? CH / 2 : CH;
     static constexpr int kBytesX = TK * 256, kBytesW = CH * 128, kStep = kBytesX + kBytesW;
     static constexpr int kBytesS = 2 * SUBS * CH * 4;  // a step's scales, as f32
     static constexpr int kLds = 2 * (kStep + kBytesS);
     static constexpr int XJ = TK / 4 / NW, WJ = CH / 8 / NW;  // direct loads a wave and step
+    static constexpr int SJ = 2 * CH / (NW * kWave);  // channels' halves whose scales a thread loads
     static constexpr int PER = 4 / SUBS;                      // products of a group within a half
-    static_assert(NW * kWave == 2 * CH, "a thread loads the scales of a channel and half");
-    static_assert(TK % (4 * NW) == 0 && CH % (8 * NW) == 0 && kLds <= 160 * 1024, "whole loads a wave");
+    static_assert(TK % (4 * NW) == 0 && CH % (8 * NW) == 0 && 2 * CH % (NW * kWave) == 0 && (!GATED || WT == 2), "whole loads a wave");
+    static_assert(kLds * kShape.split == kShape.lds(SUBS) && kShape.lds(SUBS) <= 160 * 1024, "the launch's LDS");
     static __device__ constexpr int piece(int i, int h) { return SUBS == 4 ? 2 * i + h : 4 * (i >> 1) + 2 * h + (i & 1); }
 };
 
@@ -52,7 +54,7 @@ template <typename C, int ST>
 struct I4TileLoop {
     const I4Product &p;
     char *lds;
-    int lane, wave, wm, wn, half, m;
+    int lane, wave, wm, wn, half, m;  // wave: of the tile
     int64_t t0, n0;    // first token (routed row), first output channel of the workgroup
     int rows, expert;  // rows of the tile
 
@@ -68,16 +70,21 @@ struct I4TileLoop {
     __device__ __forceinline__ const int32_t *matrix(bool up) const { return up ? p.w_up : p.w; }
     __device__ __forceinline__ const void *scales(bool up) const { return up ? p.up_scale : p.w_scale; }
 
-    // row_of(r): the row of x for row r of the tile.
+    // Waves of one tile meet; a wave with a tile of its own goes on.
+    __device__ __forceinline__ static void meet() {
+        if constexpr (C::NW > 1) barrier();
+    }
+
+    // Adds the products of the steps begin .. begin + steps - 1, and where `tail` those
+    // past the last whole step.  row_of(r): the row of x for row r of the tile.
     template <typename RowOf>
-    __device__ __forceinline__ void run(RowOf &&row_of) {
+    __device__ __forceinline__ void run(int begin, int steps, bool tail, RowOf &&row_of) {
 #pragma unroll
         for (int x = 0; x < C::XT; ++x)
 #pragma unroll
             for (int w = 0; w < C::WT; ++w)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[x][w][r] = 0.0f;
-        const int steps = p.chunks / 8;
         const int64_t kb = (int64_t)p.chunks * 32;
         const char *from_x[C::XJ], *from_w[C::WJ];
 #pragma unroll
@@ -95,26 +102,37 @@ struct I4TileLoop {
         auto load = [&](auto at_j, int64_t s, int place) {
             constexpr int j = decltype(at_j)::value, k = j < C::XJ ? 0 : j - C::XJ;
             const int to = at + (place & 1) * C::kStep;
-            if constexpr (j < C::XJ) gather_to_lds(from_x[j] + s * 256, to + C::NW * j * 1024);
-            else gather_to_lds(from_w[k] + s * 128, to + C::kBytesX + C::NW * k * 1024);
+            if constexpr (j < C::XJ) gather_to_lds(from_x[j] + (begin + s) * 256, to + C::NW * j * 1024);
+            else gather_to_lds(from_w[k] + (begin + s) * 128, to + C::kBytesX + C::NW * k * 1024);
         };
         // Scales: read by every wave that uses them, a line for each lane and two bytes, they
         // took 200 of 1200 us at 4096 x 8192 x 28672.  Each thread reads those of one channel
         // and half of a step, and they wait in LDS.
         typedef typename ElementOf<ST>::type Scale;
         typedef Scale Scales __attribute__((ext_vector_type(C::SUBS), aligned(sizeof(Scale))));
-        const int ch = threadIdx.x >> 1, my_half = threadIdx.x & 1;
-        const Scale *my_scales = (const Scale *)scales(is_up(ch)) + weight_row(ch) * p.groups;
         float *const held = (float *)(lds + 2 * C::kStep);
-        Scales coming;
+        const Scale *my_scales[C::SJ];
+        Scales coming[C::SJ];
+        const int tid = wave * kWave + lane;
+#pragma unroll
+        for (int j = 0; j < C::SJ; ++j) {
+            const int r = (tid + j * C::NW * kWave) >> 1;
+            my_scales[j] = (const Scale *)scales(is_up(r)) + weight_row(r) * p.groups;
+        }
         auto fetch_scales = [&](int s) {
-            s = min(s, steps - 1);
-            coming = *(const Scales *)(my_scales + (C::SUBS > 1 ? (2 * s + my_half) * C::SUBS : (8 * s + 4 * my_half) >> p.chunk_shift));
+            s = begin + min(s, steps - 1);
+            const int h = tid & 1, g = C::SUBS > 1 ? (2 * s + h) * C::SUBS : (8 * s + 4 * h) >> p.chunk_shift;
+#pragma unroll
+            for (int j = 0; j < C::SJ; ++j) coming[j] = *(const Scales *)(my_scales[j] + g);
         };
         auto keep_scales = [&](int s) {
-            float *to = held + ((s & 1) * 2 + my_half) * (C::SUBS * C::CH) + ch;
 #pragma unroll
-            for (int u = 0; u < C::SUBS; ++u) to[u * C::CH] = (float)coming[u];
+            for (int j = 0; j < C::SJ; ++j) {
+                const int r = (tid + j * C::NW * kWave) >> 1;
+                float *to = held + ((s & 1) * 2 + (tid & 1)) * (C::SUBS * C::CH) + r;
+#pragma unroll
+                for (int u = 0; u < C::SUBS; ++u) to[u * C::CH] = (float)coming[j][u];
+            }
         };
         if (steps > 0) {
             float scale[C::WT][C::SUBS];
@@ -124,10 +142,10 @@ struct I4TileLoop {
             each_index<C::XJ + C::WJ>([&](auto j) { load(j, min(1, steps - 1), 1); });
             wait_loads<C::XJ + C::WJ>();
             wait_lds();
-            barrier();
+            meet();
             constexpr int WL = C::SUBS == 4 ? 4 : 2;
             int4v a[4], raw[C::WT][WL], b[C::WT][4];
-            const char *base_x = lds + (wn * C::XT * 32 + m) * 256, *base_w = lds + C::kBytesX + (wm * 64 + m) * 128;
+            const char *base_x = lds + (wn * C::XT * 32 + m) * 256, *base_w = lds + C::kBytesX + (wm * C::WT * 32 + m) * 128;
             // fragments of half h (0, 1) of the step at that place
             auto read_a = [&](int place, int h, int x, int i) {
                 a[i] = *(const int4v *)(base_x + place + x * 8192 + (((8 * h + C::piece(i, half)) ^ (m & 15)) << 4));
@@ -158,7 +176,7 @@ struct I4TileLoop {
                 const int place = (s & 1) * C::kStep, other = C::kStep - place;
                 const int64_t after = min(s + 2, steps - 1);  // past the end the last step again
                 fetch_scales(s + 1);
-                const float *my = held + (s & 1) * (2 * C::SUBS * C::CH) + wm * 64 + m;
+                const float *my = held + (s & 1) * (2 * C::SUBS * C::CH) + wm * C::WT * 32 + m;
                 // units of PER products that end a group's part, block by block; while one is
                 // multiplied the sums of the one before are converted, scaled and added, and in
                 // the last blocks the next half's fragments are read and unpacked into the
@@ -184,7 +202,7 @@ struct I4TileLoop {
                                     keep_scales(s + 1);
                                     wait_loads<0>();
                                     wait_lds();
-                                    barrier();
+                                    meet();
                                 }
                                 read_w(then, 1 - h);
                             }
@@ -219,7 +237,7 @@ struct I4TileLoop {
         }
         // the rest of k, up to seven times 32 elements, in parts of a group and at most 128
         constexpr int kPart = 4 / C::SUBS;
-        for (int c0 = 8 * steps; c0 < p.chunks; c0 += kPart) {
+        for (int c0 = tail ? p.chunks / 8 * 8 : p.chunks; c0 < p.chunks; c0 += kPart) {
             const int c1 = min(c0 + kPart, p.chunks), g = c0 >> p.chunk_shift;
 #pragma unroll
             for (int x = 0; x < C::XT; ++x) {
@@ -228,13 +246,13 @@ struct I4TileLoop {
                 for (int c = c0; c < c1; ++c)
 #pragma unroll
                     for (int w = 0; w < C::WT; ++w) {
-                        const int64_t row = weight_row(wm * 64 + w * 32 + m);
+                        const int64_t row = weight_row((wm * C::WT + w) * 32 + m);
                         const int4v v = ((const int4v *)matrix(C::GATED && w))[row * p.chunks + c];
                         sum[w] = __builtin_amdgcn_mfma_i32_32x32x32_i8(xr[2 * c + half], half ? i4_high(v) : i4_low(v), sum[w], 0, 0, 0);
                     }
 #pragma unroll
                 for (int w = 0; w < C::WT; ++w) {
-                    const float scale = scale_at<ST>(scales(C::GATED && w), weight_row(wm * 64 + w * 32 + m) * p.groups + g);
+                    const float scale = scale_at<ST>(scales(C::GATED && w), weight_row((wm * C::WT + w) * 32 + m) * p.groups + g);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) acc[x][w][r] = __builtin_fmaf((float)sum[w][r], scale, acc[x][w][r]);
                 }
@@ -242,29 +260,29 @@ struct I4TileLoop {
         }
     }
 
-    // scale_of(r): x_scale of row r of the tile.
-    template <typename ScaleOf>
-    __device__ __forceinline__ void store(int type, ScaleOf &&scale_of) {
+    // Stores the sums r0 .. r0 + N - 1 of each block.  scale_of(r): x_scale of row r of the tile.
+    template <int N, typename ScaleOf>
+    __device__ __forceinline__ void store(int type, int r0, ScaleOf &&scale_of) {
 #pragma unroll
         for (int x = 0; x < C::XT; ++x) {
             const int first = (wn * C::XT + x) * 32;
             if (first >= rows) return;
             const float xs = scale_of(min(first + m, rows - 1));
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = 8 * (r >> 2) + 4 * half + (r & 3);
+            for (int e = 0; e < N; ++e) {
+                const int r = r0 + e, row = 8 * (r >> 2) + 4 * half + (r & 3);
                 const float scale = __shfl(xs, row);
                 const int64_t out = (t0 + first + row) * p.out_stride;
                 const bool live = first + row < rows;
                 if constexpr (C::GATED) {
                     const int64_t n = n0 + wm * 32 + m;
-                    const float y = act_value(p.act, acc[x][0][r] * kI4Unit * scale) * (acc[x][1][r] * kI4Unit * scale);
+                    const float y = act_value(p.act, acc[x][0][e] * kI4Unit * scale) * (acc[x][1][e] * kI4Unit * scale);
                     if (live && n < p.rows) store1(p.out, type, out + n, y);
                 } else {
 #pragma unroll
                     for (int w = 0; w < C::WT; ++w) {
-                        const int64_t n = n0 + wm * 64 + w * 32 + m;
-                        float y = acc[x][w][r] * kI4Unit * scale;
+                        const int64_t n = n0 + (wm * C::WT + w) * 32 + m;
+                        float y = acc[x][w][e] * kI4Unit * scale;
                         if (live && n < p.rows) {
                             if (p.bias) y = y + p.bias[(int64_t)expert * p.rows + n];
                             store1(p.out, type, out + n, y);

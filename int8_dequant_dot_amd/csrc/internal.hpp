@@ -655,9 +655,82 @@ struct GroupArgs {
 // by expert, there plain or gated.
 enum I4Form { kI4Dense, kI4Routed, kI4RoutedGated };
 constexpr int64_t kI4MaxK = 131040, kI4MaxExperts = 1024;
-constexpr int kI4Waves = 4;
+// Groups within 128 elements of k.
 constexpr int i4_subs(int chunk_shift) { return chunk_shift >= 2 ? 1 : chunk_shift == 1 ? 2 : 4; }
-constexpr bool i4_use_tiles(int64_t tokens, int64_t experts) { return tokens > (experts > 0 ? 32 * experts : 32); }
+constexpr int kI4StreamWaves = 4, kI4StreamLoads = 8;
+// Token slots (4 or 8, a token takes subs of them) of the kernel for few tokens, 0: too
+// many tokens for it.  Of experts it takes those with up to 4 slots on average: with 6
+// rows each, 64 experts x 2048 x 2048 took 50 us so and 33 us in tiles, while at 28672 x
+// 8192, dense, 6 tokens took 26 us so and 38 us in tiles.
+constexpr int i4_stream_slots(int64_t tokens, int64_t experts, int subs) {
+    const int64_t each = experts > 0 ? ceil_of(tokens, tokens < experts ? tokens : experts) : tokens;
+    return each * subs <= 4 ? 4 : experts == 0 && each * subs <= 8 ? 8 : 0;
+}
+
+// Tiles of the 4-bit products: xt x wt blocks of 32 tokens x 32 channels a wave, wn x wm
+// waves, or `split` waves that share a block and split k.
+struct I4TileShape {
+    int xt, wn, wm, wt, split;
+    double step_us[3], work_us[3];  // for 1, 2 and 4 groups in 128
+    constexpr int tokens() const { return 32 * xt * wn; }
+    constexpr int channels() const { return 32 * wm * wt; }
+    constexpr int waves() const { return wn * wm * split; }
+    constexpr int lds(int subs) const { return 2 * split * (tokens() * 256 + channels() * (128 + 8 * subs)); }
+};
+constexpr int kI4TileCount = 4;
+constexpr I4TileShape kI4Tiles[kI4TileCount] = {
+    {2, 2, 4, 2, 1, {2.3, 2.6, 4.4}, {2.3, 2.6, 4.4}}, {1, 2, 2, 2, 1, {1.2, 1.4, 2.4}, {0.9, 1.1, 1.6}},
+    {1, 1, 4, 1, 1, {0.85, 1.0, 1.4}, {0.5, 0.6, 0.9}}, {1, 1, 1, 1, 4, {1.2, 1.4, 1.7}, {1.2, 1.4, 1.7}}};
+// A gated wave has a block of either projection.
+constexpr I4TileShape i4_tile_shape(int shape, bool gated) {
+    I4TileShape t = kI4Tiles[shape];
+    if (gated && t.wt == 1) {
+        t.wt = 2;
+        if (t.wm > 1) t.wm /= 2;
+    }
+    return t;
+}
+constexpr int64_t i4_tile_rows(int64_t tokens, int64_t experts, int size) {  // tiles of tokens, at most
+    return experts > 0 ? tokens / size + (tokens < experts ? tokens : experts) : ceil_of(tokens, size);
+}
+// The tile shape (an index of kI4Tiles) with the least estimated time: a round of r
+// workgroups a CU takes, for each step of 256, the shape's latency or r times its work
+// (us, measured), whichever is longer; the launch its rounds, or the memory's time for
+// the weights at 6 TB/s.  Routed tiles are counted as if each expert's last were half
+// full, and take longer, since few of them share weights; gated waves of the last
+// two shapes have twice the work.  Over 178 sizes (500 to 28672 channels, 6 to 2000 tokens or 6 to 250
+// rows an expert, groups of 32 and 128) the choice took 3 % longer than the fastest.
+constexpr int i4_tile_choice(int64_t rows, int64_t k, int64_t tokens, int64_t experts, bool gated, int subs) {
+    int best = 0;
+    double best_us = 0;
+    for (int i = 0; i < kI4TileCount; ++i) {
+        const I4TileShape t = i4_tile_shape(i, gated);
+        const int at = subs == 1 ? 0 : subs == 2 ? 1 : 2;
+        double slower = experts == 0 ? 1 : i == 0 ? 1.5 : 1.25;
+        if (gated && i >= 2) slower *= subs == 1 ? 1.3 : 1.7;
+        const int64_t live = tokens < experts ? tokens : experts;
+        int64_t tiles = experts > 0 ? tokens / t.tokens() + live / 2 : ceil_of(tokens, t.tokens());
+        if (tiles < live) tiles = live;
+        tiles *= ceil_of(rows, t.channels() / (gated ? 2 : 1));
+        const int resident = 160 * 1024 / t.lds(subs);
+        const int64_t round = 256 * resident, full = tiles / round, rest = ceil_of(tiles % round, 256);
+        double us = 0;
+        for (int last = 0; last < 2; ++last) {
+            const double r = last ? (double)rest : (double)resident, times = last ? (rest > 0) : (double)full;
+            const double work = r * t.work_us[at] * slower;
+            const double step = work > t.step_us[at] * slower ? work : t.step_us[at] * slower;
+            us += times * (step * (double)k / (256 * t.split) + 3);
+        }
+        const double memory = (double)(experts > 0 ? live : 1) * (double)rows * (gated ? 2 : 1) * (double)k / 12e6;
+        if (memory > us) us = memory + 0.1 * us;
+        if (i == 0 || us < best_us) {
+            best = i;
+            best_us = us;
+        }
+    }
+    return best;
+}
+
 struct I4Product {
     const int32_t *w;       // [experts][rows][k / 8]
     const void *w_scale;    // scale type [experts][rows][groups]

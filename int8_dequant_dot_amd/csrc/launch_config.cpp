@@ -216,12 +216,22 @@ template <bool ROUTED, bool GATED>
 int geo_i4(const int64_t *w, loom_launch_config *c) {
     if (w[0] < 0 || w[1] < 0 || w[1] > kI4MaxK || w[2] < 0 || w[3] < 32) return LOOM_ERR_RANGE;
     if (ROUTED && (w[4] < 1 || w[4] > kI4MaxExperts)) return LOOM_ERR_RANGE;
-    const bool big = i4_use_tiles(w[2], ROUTED ? w[4] : 0);
-    const int64_t tokens = big ? 128 : 32, channels = big ? (GATED ? 128 : 256) : 32 * kI4Waves;
-    const int64_t tiles = ROUTED ? w[2] / tokens + (w[2] < w[4] ? w[2] : w[4]) : ceil_div(w[2], tokens);
+    const int64_t experts = ROUTED ? w[4] : 0;
+    int shift = 0;  // log2 of a group's 32-element chunks
+    while (shift < 12 && (int64_t(64) << shift) <= w[3]) ++shift;
+    const int subs = i4_subs(shift), slots = i4_stream_slots(w[2], experts, subs);
+    int64_t tokens, channels, waves, lds;  // of a workgroup
+    if (slots) {
+        tokens = slots / subs, channels = kI4StreamLoads * (GATED ? 2 : 4), waves = kI4StreamWaves;
+        lds = waves * slots * 16 * kI4StreamLoads;
+    } else {
+        const I4TileShape t = i4_tile_shape(i4_tile_choice(w[0], w[1], w[2], experts, GATED, subs), GATED);
+        tokens = t.tokens(), channels = t.channels() / (GATED ? 2 : 1), waves = t.waves(), lds = t.lds(subs);
+    }
+    const int64_t tiles = i4_tile_rows(w[2], experts, (int)tokens);
     const int64_t blocks = ceil_div(w[0], channels);
     if (blocks > 0 && tiles > kMaxGridWorkItems / blocks) return LOOM_ERR_RANGE;
-    return set(c, tiles * blocks, (big ? 8 : kI4Waves) * kSubgroupSize, big ? 160 * 1024 : 0);
+    return set(c, tiles * blocks, (uint32_t)(waves * kSubgroupSize), (uint32_t)lds);
 }
 
 struct Export {
