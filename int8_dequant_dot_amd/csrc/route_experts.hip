@@ -6,8 +6,10 @@
 //     w = s[ids], divided by their sum where renormalised, times scale
 //
 // Ties go to the lower index.  Neighbouring choices may differ by less than a
-// step of f32, so wherever a choice is computed (and is not a logit itself) it
-// is computed and compared in 64 bits; weights are f32.
+// step of f32, so wherever a choice is computed (and is not a logit itself) its
+// order is that of its 64-bit value: waves whose f32 choices lie apart by more
+// than their error are done with those, the few others compute them again in 64
+// bits.  Weights are f32.
 #include <type_traits>
 
 #include "ffn_common.hpp"
@@ -70,104 +72,507 @@ __device__ __forceinline__ float relative_score(int score, float l, bool live, f
 }
 
 // ---------------------------------------------------------------- the router
-// 2^LOG lanes hold a token, lane i the experts i, i + 2^LOG, ..: R of them.
-template <typename C, int LOG, int R>
-__global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a) {
-    constexpr int L = 1 << LOG, PER = kRouteWaves * kWave / L;  // tokens of a workgroup
-    const int sub = threadIdx.x % L, slot = threadIdx.x / L;
+// 2^LOG lanes hold a token, R experts a lane, V neighbours at a time: its r-th is
+// expert_at(r).  All that a token needs of others is within its wave.
+template <int LOG, int R>
+struct Held {
+    static constexpr int L = 1 << LOG, V = R % 4 == 0 ? 4 : 1;
+    static __device__ __forceinline__ int expert_at(int r, int sub) { return r / V * (L * V) + r % V + sub * V; }
+};
+
+// A row's values, `other` past its end; its rows may be aligned to the element only.
+template <int LOG, int R, typename T>
+__device__ __forceinline__ void load_row(const T *row, int n, int sub, float past, float (&l)[R]) {
+    typedef Held<LOG, R> H;
+    typedef T Run __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+#pragma unroll
+    for (int r = 0; r < R; r += H::V) {
+        const int e = H::expert_at(r, sub);
+        if (H::V == 4 && e + 4 <= n) {
+            const Run v = *(const Run *)(row + e);
+#pragma unroll
+            for (int i = 0; i < H::V; ++i) l[r + i] = (float)v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < H::V; ++i) l[r + i] = e + i < n ? (float)row[e + i] : past;
+        }
+    }
+}
+template <int LOG, int R>
+__device__ __forceinline__ void load_logits(const void *l, int type, int64_t at, int n, int sub, float past, float (&to)[R]) {
+    if (type == LOOM_F32) load_row<LOG, R>((const float *)l + at, n, sub, past, to);
+    else if (type == LOOM_F16) load_row<LOG, R>((const _Float16 *)l + at, n, sub, past, to);
+    else load_row<LOG, R>((const __bf16 *)l + at, n, sub, past, to);
+}
+
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+// f32 values as whole numbers of the same order (-0 as 0), whose maxima and minima
+// need no care for NaNs and fold into cross-lane moves.
+__device__ __forceinline__ int key_of(float v) {
+    const int b = __builtin_bit_cast(int, v + 0.0f);
+    return b ^ (int)((uint32_t)(b >> 31) >> 1);
+}
+__device__ __forceinline__ float of_key(int k) { return __builtin_bit_cast(float, k ^ (int)((uint32_t)(k >> 31) >> 1)); }
+constexpr int kNone = (int)0x807FFFFF;  // key_of(-infinity)
+
+// The two largest of a lane's and of 2^STEPS lanes' values.
+__device__ __forceinline__ void keep_two(int v, int &first, int &second) {
+    second = max(min(v, first), second);
+    first = max(v, first);
+}
+template <int STEPS, int S = 0>
+__device__ __forceinline__ void merge_two(int &first, int &second) {
+    if constexpr (S < STEPS) {
+        const int a = other<S>(first), b = other<S>(second);
+        second = max(max(second, b), min(first, a));
+        first = max(first, a);
+        merge_two<STEPS, S + 1>(first, second);
+    }
+}
+
+// Takes the choices of all but the best groups away: a group's value is its largest
+// choice, or the sum of its two largest, and a group stays while fewer than top_groups
+// are better.  margin: how far the worst of those that stay lies above the best of
+// the others (groups without a choice apart: it does not matter whether they stay).
+// room: LDS of this token, experts + groups values.
+template <int LOG, int R>
+__device__ __forceinline__ void best_groups(const RouteArgs &a, int sub, float *room, int (&c)[R], float &margin) {
+    typedef Held<LOG, R> H;
+    constexpr int L = H::L, B = (R + 3) / 4;
+    const int size = a.experts / a.groups;
+    int *const ranks = (int *)room + a.experts;
+    auto value = [&](int first, int second) {
+        return a.group_top > 1 && second > kNone ? key_of(of_key(first) + of_key(second)) : first;
+    };
+    int worst = 0x7FFFFFFF, best = kNone;
+    auto weigh = [&](bool stays, int mine) {
+        if (mine > kNone) {
+            worst = stays ? min(worst, mine) : worst;
+            best = stays ? best : max(best, mine);
+        }
+    };
+    if (H::V == 4 && size >= 4 && size <= 4 * L && (size & (size - 1)) == 0) {
+        // groups of 4, 8, .. neighbouring experts lie on 1, 2, .. neighbouring lanes
+        const int shift = __builtin_ctz(size);
+        int mine[B], group[B], better[B] = {};
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            int first = kNone, second = kNone;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) keep_two(c[min(4 * b + i, R - 1)], first, second);
+            switch (shift) {
+                case 2: break;
+                case 3: merge_two<1>(first, second); break;
+                case 4: merge_two<2>(first, second); break;
+                case 5: merge_two<3>(first, second); break;
+                case 6: merge_two<4>(first, second); break;
+                case 7: merge_two<(LOG >= 5 ? 5 : 0)>(first, second); break;
+                default: merge_two<(LOG >= 6 ? 6 : 0)>(first, second);
+            }
+            mine[b] = value(first, second);
+            const int e = H::expert_at(4 * b, sub);
+            group[b] = e >> shift;
+            if (e < a.experts && (e & (size - 1)) == 0) ranks[group[b]] = mine[b];
+        }
+        wave_fence();
+        for (int o = 0; o < a.groups; ++o) {
+            const int that = ranks[o];
+#pragma unroll
+            for (int b = 0; b < B; ++b) better[b] += that - (o >= group[b]) >= mine[b];  // equal and before it, or greater
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const bool stays = better[b] < a.top_groups;
+            weigh(stays, mine[b]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * b + i < R) c[4 * b + i] = stays ? c[4 * b + i] : kNone;
+        }
+    } else {
+        int *const values = (int *)room;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (H::expert_at(r, sub) < a.experts) values[H::expert_at(r, sub)] = c[r];
+        wave_fence();
+        for (int g = sub; g < a.groups; g += L) {
+            int first = kNone, second = kNone;
+            for (int i = 0; i < size; ++i) keep_two(values[g * size + i], first, second);
+            ranks[g] = value(first, second);
+        }
+        wave_fence();
+        // each group's verdict, then each expert's
+        for (int g0 = 0; g0 < a.groups; g0 += L) {
+            const int g = g0 + sub;
+            if (g < a.groups) {
+                const int mine = ranks[g];
+                int better = 0;
+                for (int o = 0; o < a.groups; ++o) better += ranks[o] - (o >= g) >= mine;
+                weigh(better < a.top_groups, mine);
+                if (better >= a.top_groups)
+                    for (int i = 0; i < size; ++i) values[g * size + i] = kNone;
+            }
+        }
+        wave_fence();
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (H::expert_at(r, sub) < a.experts) c[r] = values[H::expert_at(r, sub)];
+    }
+    margin = of_key(fold_min<LOG>(worst)) - of_key(fold_max<LOG>(best));
+    wave_fence();  // the room may be written again
+}
+
+// The top_k largest choices, lane i keeping the i-th's expert, -1 where there is none.
+// Equal ones in the order of their experts.
+template <int LOG, int R>
+__device__ __forceinline__ int largest(int top_k, int sub, int (&c)[R]) {
+    typedef Held<LOG, R> H;
+    int id = -1;
+    for (int i = 0; i < top_k; ++i) {
+        int best = kNone;
+#pragma unroll
+        for (int r = 0; r < R; ++r) best = max(best, c[r]);
+        best = fold_max<LOG>(best);
+        int at = 0x3FFFFFFF;
+#pragma unroll
+        for (int r = R - 1; r >= 0; --r) at = c[r] == best ? H::expert_at(r, 0) : at;
+        at = best > kNone ? fold_min<LOG>(at + sub * H::V) : -1;
+        const int mine = at - sub * H::V;
+#pragma unroll
+        for (int r = 0; r < R; ++r) c[r] = H::expert_at(r, 0) == mine ? kNone : c[r];
+        if (sub == i) id = at;
+    }
+    return id;
+}
+
+// Keys in falling order, by comparators; of 16 only the first 8.
+__device__ __forceinline__ void order(int &a, int &b) {
+    const int low = min(a, b);
+    a = max(a, b);
+    b = low;
+}
+__device__ __forceinline__ void sort8(int *h) {
+    order(h[0], h[1]), order(h[2], h[3]), order(h[4], h[5]), order(h[6], h[7]);
+    order(h[0], h[2]), order(h[1], h[3]), order(h[4], h[6]), order(h[5], h[7]);
+    order(h[1], h[2]), order(h[5], h[6]);
+    order(h[0], h[4]), order(h[1], h[5]), order(h[2], h[6]), order(h[3], h[7]);
+    order(h[2], h[4]), order(h[3], h[5]);
+    order(h[1], h[2]), order(h[3], h[4]), order(h[5], h[6]);
+}
+template <int R>
+__device__ __forceinline__ void sort_heads(int (&k)[R]) {
+    if constexpr (R == 4) {
+        order(k[0], k[1]), order(k[2], k[3]), order(k[0], k[2]), order(k[1], k[3]), order(k[1], k[2]);
+    } else if constexpr (R >= 8) {
+        sort8(k);
+        if constexpr (R == 16) {
+            sort8(k + 8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) k[i] = max(k[i], k[15 - i]);
+#pragma unroll
+            for (int d = 4; d > 0; d /= 2)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (!(i & d)) order(k[i], k[i + d]);
+        }
+    }
+}
+
+// The top_k largest choices by sorted lists: each lane sorts its keys once, and a step
+// takes the largest head of a token's lanes, whose lane writes it down.  (Searching every
+// key in every step took 1.2 of the router's 1.6 thousand instructions a wave at 65536 x
+// 256, top 8; to hand each step's expert to all lanes 0.35 of them.)
+//
+// EXACT: keys of 16-bit logits, whose low bits hold the expert, so that they are all
+// different and in the order wanted.  Otherwise the low bits hold which of the lane's
+// it was, and choices that are not `gap` and the bits so lost apart may be in either order.
+// lost: a choice may be missing.  room: LDS of this token, 2 L words.
+template <bool EXACT, int LOG, int R>
+struct SortedChoice {
+    typedef Held<LOG, R> H;
+    static constexpr int D = R < 8 ? R : 8, LOW = EXACT ? H::L * R - 1 : R - 1;
+    int h[R], popped = 0, taken = 0;
+    bool lost = false;
+    int *const room;
+
+    __device__ __forceinline__ SortedChoice(const int (&key)[R], int sub, int *room_) : room(room_) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            h[r] = key[r] == kNone ? kNone : (key[r] & ~LOW) | (LOW - (EXACT ? H::expert_at(r, sub) : r));
+        sort_heads(h);
+        room[sub] = kNone;
+        wave_fence();
+    }
+    // Writes down choices up to `count`, at most L.
+    __device__ __forceinline__ void take(int count, int sub) {
+        for (; taken < count; ++taken) {
+            const int best = fold_max<LOG>(h[0]);
+            const bool some = best > kNone, hit = some && h[0] == best;
+            if (hit) {
+                room[taken] = best;
+                if (!EXACT) room[H::L + taken] = sub;
+            }
+            if (!EXACT) {
+                const uint64_t hits = __builtin_amdgcn_ballot_w64(hit), lanes = __builtin_amdgcn_ballot_w64(some);
+                if (__builtin_popcountll(hits) != __builtin_popcountll(lanes) >> LOG) lost = true;  // two alike
+            }
+#pragma unroll
+            for (int i = 0; i < D; ++i) h[i] = hit ? (i + 1 < D ? h[i + 1] : kNone) : h[i];
+            popped += hit;
+        }
+        if (D < R && popped >= D) lost = true;  // this lane's list is used up, its keys may not be
+        wave_fence();
+    }
+    __device__ __forceinline__ float value(int i) const { return of_key(room[i] & ~LOW); }
+    __device__ __forceinline__ bool some(int i) const { return room[i] > kNone; }
+    static __device__ __forceinline__ bool apart(float high, float low, float gap) {
+        return high - low > gap + 0x1p-19f * (fabsf(high) + fabsf(low));
+    }
+    // Whether the choice after lane sub's lies apart from it, or there is none.
+    __device__ __forceinline__ bool clear(int sub, float gap) const {
+        return sub + 1 >= taken || !some(sub + 1) || apart(value(sub), value(sub + 1), gap);
+    }
+    // Lane sub's choice, -1 where there is none.
+    __device__ __forceinline__ int expert(int sub) const {
+        const int best = room[sub], low = LOW - (best & LOW);
+        const int id = sub < taken && best > kNone ? (EXACT ? low : H::expert_at(low, room[H::L + sub])) : -1;
+        return id;
+    }
+};
+
+// Choices of a sigmoid and a bias that lie too close together in f32: lane i has
+// candidate i of `count`, which are put in the order of their 64-bit values.
+template <int LOG>
+__device__ __forceinline__ int order_candidates(const RouteArgs &a, int64_t row, int sub, int count, int id, double *room) {
+    const double none = -(double)kInf;
+    double mine = none;
+    if (id >= 0 && sub < count)
+        mine = 1.0 / (1.0 + exp(-(double)load_logit(a.logits, a.type, row + id))) + (double)a.bias[id];
+    room[sub] = mine;
+    wave_fence();
+    int rank = 0;
+    for (int o = 0; o < count; ++o) {
+        const int e = __shfl(id, o, 1 << LOG);
+        const double that = room[o];
+        rank += that > mine || (that == mine && that > none && e < id);
+    }
+    wave_fence();
+    int *const out = (int *)room;
+    out[sub] = -1;
+    wave_fence();
+    if (mine > none) out[rank] = id;
+    wave_fence();
+    id = out[sub];
+    wave_fence();
+    return id;
+}
+
+// The same choice from 64-bit values, for tokens whose f32 ones lie too close together.
+// A token in some hundreds needs it, so it takes few registers at a time, and a wave that
+// does takes about 7 us.  room: experts + groups values.
+template <int LOG, int R>
+__device__ __forceinline__ int choose_wide(const RouteArgs &a, int sub, float top, const float (&l)[R], const float (&bias)[R],
+                                           double *room) {
+    typedef Held<LOG, R> H;
+    constexpr int L = H::L;
+    const double none = -(double)kInf;
+    double sum = 0.0, c[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int e = H::expert_at(r, sub);
+        const double x = exp(a.score == LOOM_SIGMOID ? -(double)l[r] : (double)l[r] - (double)top);
+        if (e < a.experts) room[e] = a.score == LOOM_SIGMOID ? 1.0 / (1.0 + x) : x;
+        sum += x;
+        __builtin_amdgcn_sched_barrier(0);  // one exponential after the other
+    }
+    sum = a.score == LOOM_SIGMOID ? 1.0 : fold_sum<LOG>(sum);
+    wave_fence();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int e = H::expert_at(r, sub);
+        if (e < a.experts) room[e] = l[r] == -kInf ? none : room[e] / sum + (double)bias[r];
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    wave_fence();
+    if (a.groups > 1) {
+        const int size = a.experts / a.groups;
+        double *const ranks = room + a.experts;
+        for (int g = sub; g < a.groups; g += L) {
+            double first = none, second = none;
+#pragma unroll 4
+            for (int i = 0; i < size; ++i) {
+                const double v = room[g * size + i], low = v < first ? v : first;
+                second = low > second ? low : second;
+                first = v > first ? v : first;
+            }
+            ranks[g] = a.group_top > 1 && second > none ? first + second : first;
+        }
+        wave_fence();
+        for (int g = sub; g < a.groups; g += L) {
+            const double mine = ranks[g];
+            int better = 0;
+#pragma unroll 4
+            for (int o = 0; o < a.groups; ++o) better += ranks[o] > mine || (ranks[o] == mine && o < g);
+            if (better >= a.top_groups)
+                for (int i = 0; i < size; ++i) room[g * size + i] = none;
+        }
+        wave_fence();
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int e = H::expert_at(r, sub);
+        c[r] = e < a.experts ? room[e] : none;
+        if (!a.bias && c[r] > none) c[r] = (double)l[r];  // the logits order the experts
+    }
+    int id = -1;
+    for (int i = 0; i < a.top_k; ++i) {
+        double best = none;
+#pragma unroll
+        for (int r = 0; r < R; ++r) best = c[r] > best ? c[r] : best;
+        best = fold_max<LOG>(best);
+        int at = 0x3FFFFFFF;
+#pragma unroll
+        for (int r = R - 1; r >= 0; --r) at = c[r] == best ? H::expert_at(r, 0) : at;
+        at = best > none ? fold_min<LOG>(at + sub * H::V) : -1;
+        const int mine = at - sub * H::V;
+#pragma unroll
+        for (int r = 0; r < R; ++r) c[r] = H::expert_at(r, 0) == mine ? none : c[r];
+        if (sub == i) id = at;
+    }
+    wave_fence();
+    return id;
+}
+
+// The top_k largest of the logits whose keys these are.  (A top_k of all lanes leaves no
+// room for the choice behind the last.)
+template <int LOG, int R>
+__device__ __forceinline__ int largest_logits(const RouteArgs &a, int sub, int bad, int (&c)[R], int *room) {
+    int id;
+    bool sure;
+    if (a.type == LOOM_F32) {
+        SortedChoice<false, LOG, R> sorted(c, sub, room);
+        sorted.take(min(a.top_k + 1, 1 << LOG), sub);
+        id = sorted.expert(sub);
+        sure = !sorted.lost && a.top_k < 1 << LOG && sorted.clear(sub, 0.0f);
+    } else {
+        SortedChoice<true, LOG, R> sorted(c, sub, room);
+        sorted.take(a.top_k, sub);
+        id = sorted.expert(sub);
+        sure = !sorted.lost;
+    }
+    wave_fence();
+    if (__ballot(!sure && !bad)) id = largest<LOG, R>(a.top_k, sub, c);
+    return id;
+}
+
+template <int LOG, int R>
+__global__ __launch_bounds__(kRouteWaves * kWave, R < 16 ? 4 : 3) void route_kernel(RouteArgs given) {
+    RouteArgs a = given;
+    typedef Held<LOG, R> H;
+    constexpr int L = H::L, PER = kRouteWaves * kWave / L;  // tokens of a workgroup
+    int sub = threadIdx.x % L;
+    const int slot = threadIdx.x / L;
     extern __shared__ char lds[];
-    C *values = (C *)lds + (int64_t)slot * (a.groups > 1 ? a.experts : 0);
-    C *ranks = (C *)lds + (int64_t)PER * a.experts + slot * (a.groups > 1 ? a.groups : 0);
+    double *const room = (double *)lds + slot * route_room(a.experts, a.groups);
+    const bool sigmoid = a.score == LOOM_SIGMOID;
+    // choices, or groups' values, that are computed; else logits, which need no rounding
+    const bool computed = a.bias || (a.groups > 1 && a.group_top > 1);
+    float bias[R], largest_bias = 0.0f;
+    bool odd = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) bias[r] = 0.0f;
+    if (a.bias) {
+        load_row<LOG, R>(a.bias, a.experts, sub, 0.0f, bias);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (fabsf(bias[r]) < kInf) largest_bias = fmaxf(largest_bias, fabsf(bias[r]));
+            odd |= bias[r] != bias[r];
+        }
+        largest_bias = fold<LOG>(largest_bias, [](float x, float y) { return fmaxf(x, y); });
+    }
+    const bool any_odd = __ballot(odd);
     for (int64_t base = (int64_t)blockIdx.x * PER; base < a.tokens; base += (int64_t)gridDim.x * PER) {
         const int64_t t = base + slot < a.tokens ? base + slot : a.tokens - 1;
         const int64_t row = t * a.stride;
-        float l[R], top = -kInf;
+        // what follows from these two is computed where it is used: kept over the tokens, a
+        // mask for every expert a lane holds would fill the scalar registers
+        asm volatile("" : "+s"(a.experts), "+v"(sub));
+        float l[R];
+        load_logits<LOG, R>(a.logits, a.type, row, a.experts, sub, -kInf, l);
         int bad = 0;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int e = r * L + sub;
-            l[r] = e < a.experts ? load_logit(a.logits, a.type, row + e) : -kInf;
-            bad |= !(l[r] < kInf);
-            top = fmaxf(top, l[r]);
-        }
-        C c[R];
-        float total = 1.0f;
-        top = fold_max<LOG>(top);
-        const float from = top == -kInf ? 0.0f : top;  // no expert at all
-        if (a.score == LOOM_SOFTMAX) {
-            float sum = 0.0f;
+        for (int r = 0; r < R; ++r) bad |= !(l[r] < kInf);
+        if (any_odd) {  // a NaN bias of an expert that is not masked
 #pragma unroll
-            for (int r = 0; r < R; ++r) sum += expf(l[r] - from);
-            total = fold_sum<LOG>(sum);
-        }
-        // the choices: computed ones are 64-bit throughout
-        if constexpr (sizeof(C) == 8) {
-            double sum = 0.0;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                c[r] = a.score == LOOM_SIGMOID ? 1.0 / (1.0 + exp(-(double)l[r])) : exp((double)l[r] - (double)from);
-                if (a.score == LOOM_SOFTMAX) sum += c[r];
-            }
-            if (a.score == LOOM_SOFTMAX) sum = fold_sum<LOG>(sum);
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int e = r * L + sub;
-                if (a.score == LOOM_SOFTMAX) c[r] = c[r] / sum;
-                if (a.bias && e < a.experts) c[r] = c[r] + (double)a.bias[e];
-                bad |= e < a.experts && l[r] > -kInf && c[r] != c[r];
-                if (l[r] == -kInf) c[r] = -kInf;
-            }
-        } else {
-#pragma unroll
-            for (int r = 0; r < R; ++r) c[r] = l[r];
+            for (int r = 0; r < R; ++r) bad |= l[r] > -kInf && a.bias[H::expert_at(r, sub)] != a.bias[H::expert_at(r, sub)];
         }
         bad = fold_or<LOG>(bad);
-        if (a.groups > 1) {
-            // a lane a group: its largest values, and whether it is among the best
-            const int size = a.experts / a.groups;
-            __syncthreads();
+        float top = 0.0f, total = 1.0f, s[R];
+        if (!sigmoid && (computed || !a.renormalize)) {
+            int highest = kNone;
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r * L + sub < a.experts) values[r * L + sub] = c[r];
-            __syncthreads();
-            for (int g = sub; g < a.groups; g += L) {
-                C first = -kInf, second = -kInf;
-                for (int i = 0; i < size; ++i) {
-                    const C v = values[g * size + i];
-                    if (v > first) second = first, first = v;
-                    else if (v > second) second = v;
-                }
-                ranks[g] = a.group_top > 1 && second > -kInf ? first + second : first;
-            }
-            __syncthreads();
+            for (int r = 0; r < R; ++r) highest = max(highest, key_of(l[r]));
+            highest = fold_max<LOG>(highest);
+            top = highest == kNone ? 0.0f : of_key(highest);  // 0: no expert at all
+            float sum = 0.0f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) sum += s[r] = __builtin_amdgcn_exp2f((l[r] - top) * 1.4426950408889634f);
+            total = fold_sum<LOG>(sum);
+        }
+        int id;
+        float margin;
+        if (computed) {
+            // In f32 first.  A sigmoid's error is below 2^-22 (the exponential's relative error, (1.3 |l| + 2)
+            // 2^-24, counts s (1 - s) times, and |l| s (1 - s) < 0.23; the reciprocal's is 2^-23), a softmax's below
+            // 2^-18 of it (31 additions, the terms' 2^-22 and a mean distance of at most 7 from the largest), and
+            // the bias rounds to 2^-24 of |c|: where choices or groups lie `gap` apart their order is that of the
+            // 64-bit values.
+            const float unit = 1.0f / total;  // a softmax's largest score
+            const float gap = (sigmoid ? 0x1p-21f : unit * 0x1p-17f) + largest_bias * 0x1p-23f;
+            int choice[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int g = (r * L + sub) / size;
-                if (r * L + sub >= a.experts) continue;
-                const C mine = ranks[g];
-                int better = 0;
-                for (int o = 0; o < a.groups; ++o) better += ranks[o] > mine || (ranks[o] == mine && o < g);
-                if (better >= a.top_groups) c[r] = -kInf;
-                // without a bias the logits order a group's experts
-                else if (!a.bias) c[r] = l[r];
+                const float score = sigmoid ? loom::sigmoid(l[r]) : s[r] * unit;
+                choice[r] = l[r] == -kInf ? kNone : key_of(score + bias[r]);
             }
-        }
-        int id = -1;
-        for (int i = 0; i < a.top_k; ++i) {
-            C best = -kInf;
+            bool sure = true;
+            if (a.groups > 1) {
+                best_groups<LOG, R>(a, sub, (float *)room, choice, margin);
+                sure = margin > 2 * gap;
+            }
+            if (a.bias) {
+                typedef SortedChoice<false, LOG, R> Sorted;
+                Sorted sorted(choice, sub, (int *)room);
+                sorted.take(min(a.top_k + 1, L), sub);
+                id = sorted.expert(sub);
+                if (__ballot((sorted.lost || a.top_k == L || !sorted.clear(sub, gap)) && !bad)) {
+                    if (sigmoid && a.top_k + 4 <= L) {
+                        // three candidates more, all in the order of their 64-bit values: whoever is behind
+                        // them must lie clearly behind the last choice
+                        const int count = a.top_k + 4;
+                        sorted.take(count, sub);
+                        id = sorted.expert(sub);
+                        sure &= !sorted.lost && (!sorted.some(count - 1) ||
+                                                 Sorted::apart(sorted.value(a.top_k - 1), sorted.value(count - 1), gap));
+                        wave_fence();
+                        id = order_candidates<LOG>(a, row, sub, count, id, room);
+                    } else {
+                        sure = false;
+                    }
+                }
+                wave_fence();
+            } else {
 #pragma unroll
-            for (int r = 0; r < R; ++r) best = c[r] > best ? c[r] : best;
-            best = fold_max<LOG>(best);
-            int at = 0x7FFFFFFF;
+                for (int r = 0; r < R; ++r) choice[r] = choice[r] == kNone ? kNone : key_of(l[r]);
+                id = largest_logits<LOG, R>(a, sub, bad, choice, (int *)room);
+            }
+            if (__ballot(!sure && !bad)) id = choose_wide<LOG, R>(a, sub, top, l, bias, room);
+        } else {
+            int c[R];
 #pragma unroll
-            for (int r = R - 1; r >= 0; --r)
-                if (c[r] == best) at = r * L + sub;
-            at = fold_min<LOG>(at);
-            if (!(best > -kInf)) at = -1;
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r * L + sub == at) c[r] = -kInf;
-            if (sub == i) id = at;
+            for (int r = 0; r < R; ++r) c[r] = key_of(l[r]);
+            if (a.groups > 1) best_groups<LOG, R>(a, sub, (float *)room, c, margin);
+            id = largest_logits<LOG, R>(a, sub, bad, c, (int *)room);
         }
         const bool live = id >= 0 && sub < a.top_k;
         const float mine = live ? load_logit(a.logits, a.type, row + id) : 0.0f;
@@ -177,7 +582,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(RouteArgs a)
             w = relative_score<LOG>(a.score, mine, live, shift);
             w = w / fold_sum<LOG>(w);
         } else {
-            w = a.score == LOOM_SIGMOID ? 1.0f / (1.0f + expf(-mine)) : expf(mine - from) / total;
+            w = sigmoid ? 1.0f / (1.0f + expf(-mine)) : expf(mine - top) / total;
         }
         if (sub < a.top_k && base + slot < a.tokens) {
             a.ids[t * a.top_k + sub] = bad ? sub : id;
@@ -280,11 +685,8 @@ void with_lanes(int64_t tokens, int64_t experts, int64_t top_k, Use &&use) {
 hipError_t launch_route_experts(const loom_launch_config &cfg, const RouteArgs &a, hipStream_t stream) {
     const dim3 grid(cfg.workgroups[0]), block(cfg.workgroup_size[0]);
     with_lanes(a.tokens, a.experts, a.top_k, [&](auto log, auto held) {
-        constexpr int LOG = decltype(log)::value, R = decltype(held)::value;
-        if (a.bias || (a.groups > 1 && a.group_top > 1))
-            hipLaunchKernelGGL((route_kernel<double, LOG, R>), grid, block, cfg.workgroup_storage_bytes, stream, a);
-        else
-            hipLaunchKernelGGL((route_kernel<float, LOG, R>), grid, block, cfg.workgroup_storage_bytes, stream, a);
+        hipLaunchKernelGGL((route_kernel<decltype(log)::value, decltype(held)::value>), grid, block,
+                           cfg.workgroup_storage_bytes, stream, a);
     });
     return hipGetLastError();
 }
