@@ -53,13 +53,21 @@ __global__ __launch_bounds__(kGroupWaves * kWave) void group_place_kernel(GroupA
     for (int e = threadIdx.x; e <= n; e += blockDim.x) before[e] = all[e] = 0;
     __syncthreads();
     for (int64_t p = first + lane; p < last; p += kWave) atomicAdd(&next[wave][expert_of(a, p, last)], 1);
-    // counts of earlier blocks and of all (whole numbers: any order)
-    if (blocks > 1)
-        for (int64_t i = threadIdx.x; i < (int64_t)blocks * n; i += blockDim.x) {
-            const int b = (int)(i / n), e = (int)(i - (int64_t)b * n), c = a.counts[i];
-            if (c && b < (int)blockIdx.x) atomicAdd(&before[e], c);
-            if (c) atomicAdd(&all[e], c);
-        }
+    // counts of earlier blocks and of all (whole numbers: any order), a thread an expert and
+    // every blockDim / n-th block
+    if (blocks > 1) {
+        const int threads = (int)blockDim.x / n * n, step = threads / n, e = threadIdx.x % n;
+        int earlier = 0, sum = 0;
+        if ((int)threadIdx.x < threads)
+#pragma unroll 8
+            for (int b = threadIdx.x / n; b < blocks; b += step) {
+                const int c = a.counts[(int64_t)b * n + e];
+                sum += c;
+                earlier += b < (int)blockIdx.x ? c : 0;
+            }
+        if (sum) atomicAdd(&all[e], sum);
+        if (earlier) atomicAdd(&before[e], earlier);
+    }
     __syncthreads();
     // first places: the running sum over experts, 64 a wave
     int mine[(kGroupMaxExperts + kGroupWaves * kWave - 1) / (kGroupWaves * kWave)];

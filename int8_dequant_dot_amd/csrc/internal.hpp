@@ -621,6 +621,12 @@ constexpr int64_t route_room(int64_t experts, int64_t groups) { return experts +
 constexpr int route_log_lanes(int64_t tokens, int64_t experts, int64_t top_k) {
     return experts <= 256 && top_k <= 16 && tokens >= 1024 ? 4 : 6;
 }
+// Experts that a token's lanes hold, the last of them perhaps past its end.
+constexpr int64_t route_held(int64_t tokens, int64_t experts, int64_t top_k) {
+    const int log = route_log_lanes(tokens, experts, top_k);
+    const int64_t held = ceil_of(experts, int64_t(1) << log);
+    return (log == 4 ? (held <= 4 ? 4 : held <= 8 ? 8 : 16) : (held <= 1 ? 1 : held <= 4 ? 4 : 16)) << log;
+}
 struct RouteArgs {
     const void *logits;      // type[tokens], rows stride elements apart
     const float *bias;       // [experts] or NULL
@@ -636,7 +642,7 @@ struct RouteArgs {
 
 // Routes in the order of their experts: parts of at least kGroupPart routes, a
 // workgroup each, at most kGroupBlocks of them; one part needs no counts of others.
-constexpr int64_t kGroupMaxExperts = 1024, kGroupPart = 4096, kGroupBlocks = 256;
+constexpr int64_t kGroupMaxExperts = 1024, kGroupPart = 2048, kGroupBlocks = 256;
 constexpr int kGroupWaves = 16;
 constexpr int64_t group_part(int64_t pairs) {
     const int64_t even = (ceil_of(pairs, kGroupBlocks) + 1023) / 1024 * 1024;

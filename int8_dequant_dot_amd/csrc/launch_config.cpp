@@ -189,7 +189,7 @@ int geo_i8_backward(const int64_t *w, loom_launch_config *c) {
 // route_experts, route_experts_backward (tokens, experts, groups, top_k): one
 // workgroup per kRouteWaves waves of tokens, each taking every grid.x-th run once
 // the grid reaches the work-item limit (LDS: the choices of its tokens and the
-// groups' values).
+// groups' values; the gradient's chosen terms).
 template <bool BACKWARD>
 int geo_route(const int64_t *w, loom_launch_config *c) {
     if (w[0] < 0 || w[1] < 1 || w[1] > kRouteMaxExperts || w[2] < 1 || w[2] > kRouteMaxGroups || w[3] < 1 ||
@@ -197,7 +197,7 @@ int geo_route(const int64_t *w, loom_launch_config *c) {
         return LOOM_ERR_RANGE;
     const int64_t size = kRouteWaves * kSubgroupSize, per = size >> route_log_lanes(w[0], w[1], w[3]);
     return set(c, grid_stride_groups(ceil_div(w[0], per), size), (uint32_t)size,
-               BACKWARD ? 0 : (uint32_t)(8 * per * route_room(w[1], w[2])));
+               (uint32_t)(BACKWARD ? 4 * per * route_held(w[0], w[1], w[3]) : 8 * per * route_room(w[1], w[2])));
 }
 
 // group_routes(pairs, experts): one workgroup per part of group_part routes (LDS:

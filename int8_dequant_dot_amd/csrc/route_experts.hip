@@ -77,6 +77,7 @@ __device__ __forceinline__ float relative_score(int score, float l, bool live, f
 template <int LOG, int R>
 struct Held {
     static constexpr int L = 1 << LOG, V = R % 4 == 0 ? 4 : 1;
+    typedef float Values __attribute__((ext_vector_type(V)));
     static __device__ __forceinline__ int expert_at(int r, int sub) { return r / V * (L * V) + r % V + sub * V; }
 };
 
@@ -103,6 +104,32 @@ __device__ __forceinline__ void load_logits(const void *l, int type, int64_t at,
     if (type == LOOM_F32) load_row<LOG, R>((const float *)l + at, n, sub, past, to);
     else if (type == LOOM_F16) load_row<LOG, R>((const _Float16 *)l + at, n, sub, past, to);
     else load_row<LOG, R>((const __bf16 *)l + at, n, sub, past, to);
+}
+
+template <int LOG, int R, typename T>
+__device__ __forceinline__ void store_row_as(T *row, int n, int sub, const float (&y)[R]) {
+    typedef Held<LOG, R> H;
+    typedef T Run __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+#pragma unroll
+    for (int r = 0; r < R; r += H::V) {
+        const int e = H::expert_at(r, sub);
+        if (H::V == 4 && e + 4 <= n) {
+            Run v;
+#pragma unroll
+            for (int i = 0; i < H::V; ++i) v[i] = (T)y[r + i];
+            *(Run *)(row + e) = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < H::V; ++i)
+                if (e + i < n) row[e + i] = (T)y[r + i];
+        }
+    }
+}
+template <int LOG, int R>
+__device__ __forceinline__ void store_row(void *to, int type, int64_t at, int n, int sub, const float (&y)[R]) {
+    if (type == LOOM_F32) store_row_as<LOG, R>((float *)to + at, n, sub, y);
+    else if (type == LOOM_F16) store_row_as<LOG, R>((_Float16 *)to + at, n, sub, y);
+    else store_row_as<LOG, R>((__bf16 *)to + at, n, sub, y);
 }
 
 __device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
@@ -600,8 +627,11 @@ __global__ __launch_bounds__(kRouteWaves * kWave, R < 16 ? 4 : 3) void route_ker
 // An expert that was chosen several times takes the sum of its terms in order.
 template <int LOG, int R>
 __global__ __launch_bounds__(kRouteWaves * kWave) void route_backward_kernel(RouteArgs a) {
-    constexpr int L = 1 << LOG, PER = kRouteWaves * kWave / L;
+    typedef Held<LOG, R> H;
+    constexpr int L = H::L, PER = kRouteWaves * kWave / L;
+    __shared__ __align__(16) float room[PER][L * R];
     const int sub = threadIdx.x % L, slot = threadIdx.x / L;
+    float *const terms = room[slot];
     const bool whole = a.score == LOOM_SOFTMAX && !a.renormalize;
     for (int64_t base = (int64_t)blockIdx.x * PER; base < a.tokens; base += (int64_t)gridDim.x * PER) {
         const int64_t t = base + slot < a.tokens ? base + slot : a.tokens - 1;
@@ -615,27 +645,21 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_backward_kernel(Rou
 #pragma unroll
         for (int r = 0; r < R; ++r) p[r] = 0.0f;
         if (whole) {
+            load_logits<LOG, R>(a.logits, a.type, row, a.experts, sub, -kInf, p);
             float top = -kInf, sum = 0.0f;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int e = r * L + sub;
-                p[r] = e < a.experts ? load_logit(a.logits, a.type, row + e) : -kInf;
-                top = fmaxf(top, p[r]);
-            }
+            for (int r = 0; r < R; ++r) top = fmaxf(top, p[r]);
             top = fold_max<LOG>(top);
             if (top == -kInf) top = 0.0f;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                p[r] = expf(p[r] - top);
-                sum += p[r];
-            }
+            for (int r = 0; r < R; ++r) sum += p[r] = __builtin_amdgcn_exp2f((p[r] - top) * 1.4426950408889634f);
             sum = fold_sum<LOG>(sum);
             const float inverse = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-#pragma unroll
-            for (int r = 0; r < R; ++r) p[r] = p[r] * inverse;
             const float s = live ? expf(mine - top) * inverse : 0.0f;
-            all = fold_sum<LOG>(s * d);
             add = s * d;
+            all = fold_sum<LOG>(add);
+#pragma unroll
+            for (int r = 0; r < R; ++r) p[r] = -(p[r] * inverse) * all;
         } else if (a.renormalize) {
             float shift, w = relative_score<LOG>(a.score, mine, live, shift);
             const float sum = fold_sum<LOG>(w);
@@ -647,21 +671,29 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_backward_kernel(Rou
             const float e = expf(-fabsf(mine));
             add = d * e / ((1.0f + e) * (1.0f + e));
         }
-        float out[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) out[r] = whole ? -p[r] * all : 0.0f;
+        // the chosen experts' terms meet the others through LDS; of routes with one expert
+        // the first brings the sum of all in their order
+        float sum = 0.0f;
+        bool first = live;
         for (int i = 0; i < a.top_k; ++i) {
             const int e = __shfl(id, i, L);
             const float v = __shfl(add, i, L);
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r * L + sub == e) out[r] += v;
+            sum += e == id ? v : 0.0f;
+            first &= e != id || i >= sub;
         }
-        if (base + slot < a.tokens) {
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r * L + sub < a.experts) store1(a.d_logits, a.type, t * a.d_stride + r * L + sub, out[r]);
+        for (int r = 0; r < R; r += H::V) *(typename H::Values *)(terms + H::expert_at(r, sub)) = typename H::Values{};
+        wave_fence();
+        if (first) terms[id] = sum;
+        wave_fence();
+#pragma unroll
+        for (int r = 0; r < R; r += H::V) {
+            const typename H::Values v = *(const typename H::Values *)(terms + H::expert_at(r, sub));
+#pragma unroll
+            for (int i = 0; i < H::V; ++i) p[r + i] += v[i];
         }
+        wave_fence();
+        if (base + slot < a.tokens) store_row<LOG, R>(a.d_logits, a.type, t * a.d_stride, a.experts, sub, p);
     }
 }
 
@@ -669,14 +701,14 @@ template <int N> using Const = std::integral_constant<int, N>;
 template <typename Use>
 void with_lanes(int64_t tokens, int64_t experts, int64_t top_k, Use &&use) {
     const int log = route_log_lanes(tokens, experts, top_k);
-    const int held = (int)((experts + (1 << log) - 1) >> log);
+    const int64_t held = route_held(tokens, experts, top_k) >> log;
     if (log == 4) {
-        if (held <= 4) return use(Const<4>{}, Const<4>{});
-        if (held <= 8) return use(Const<4>{}, Const<8>{});
+        if (held == 4) return use(Const<4>{}, Const<4>{});
+        if (held == 8) return use(Const<4>{}, Const<8>{});
         return use(Const<4>{}, Const<16>{});
     }
-    if (held <= 1) return use(Const<6>{}, Const<1>{});
-    if (held <= 4) return use(Const<6>{}, Const<4>{});
+    if (held == 1) return use(Const<6>{}, Const<1>{});
+    if (held == 4) return use(Const<6>{}, Const<4>{});
     return use(Const<6>{}, Const<16>{});
 }
 
