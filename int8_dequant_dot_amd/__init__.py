@@ -10,6 +10,7 @@ Functions carry the C entry points' names without the ``loom_`` prefix.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch  # load torch's HIP runtime first so libloom.so binds to the same instance
@@ -503,6 +504,13 @@ def pack_int8(t: torch.Tensor) -> torch.Tensor:
 
 # ------------------------------------------------------------------ experts with 4-bit weights
 
+def _made(t, dtype, shape, numel, name, like, device):
+    """A caller's buffer, checked, or a new tensor of that shape."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    return _buffer(t, dtype, numel, name, device)
+
+
 def _score(score: str) -> int:
     if score not in SCORES:
         raise ValueError(f"score must be one of {', '.join(SCORES)}, got {score!r}")
@@ -530,12 +538,9 @@ def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax", bias
     kind, tokens, experts, stride = _logits(logits, device)
     code = _score(score)
     _buffer(bias, torch.float32, experts, "bias", device, optional=True)
-    if ids is None:
-        ids = torch.empty(tokens, max(top_k, 0), dtype=torch.int32, device=logits.device)
-    _buffer(ids, torch.int32, tokens * top_k, "ids", device)
-    if weights is None:
-        weights = torch.empty(tokens, max(top_k, 0), dtype=torch.float32, device=logits.device)
-    _buffer(weights, torch.float32, tokens * top_k, "weights", device)
+    shape = (tokens, top_k if top_k > 0 else 0)
+    ids = _made(ids, torch.int32, shape, tokens * top_k, "ids", logits, device)
+    weights = _made(weights, torch.float32, shape, tokens * top_k, "weights", logits, device)
     _check(_lib.loom_route_experts(_ptr(logits), kind, tokens, experts, stride, code, _ptr(bias), groups, top_groups,
                                    group_top, top_k, int(renormalize), scale, _ptr(ids), _ptr(weights), stream),
            "route_experts")
@@ -555,8 +560,9 @@ def route_experts_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: t
     _require(ids.dim() == 2 and ids.shape[0] == tokens and ids.is_contiguous(), "ids must be a contiguous [tokens][top_k] tensor")
     _require(d_weights.shape == ids.shape and d_weights.is_contiguous(), "d_weights must be contiguous, shaped as ids")
     if d_logits is None:
-        d_logits = torch.empty(tokens, experts, dtype=logits.dtype, device=logits.device)
-    d_stride = _rows_of(d_logits, logits.dtype, tokens, experts, "d_logits", device)
+        d_logits, d_stride = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device), experts
+    else:
+        d_stride = _rows_of(d_logits, logits.dtype, tokens, experts, "d_logits", device)
     _check(_lib.loom_route_experts_backward(_ptr(logits), kind, tokens, experts, stride, code, ids.shape[1],
                                             int(renormalize), scale, _ptr(ids), _ptr(d_weights), _ptr(d_logits),
                                             d_stride, stream), "route_experts_backward")
@@ -568,6 +574,9 @@ def group_routes_workspace(tokens: int, routes: int, experts: int) -> int:
     n = ctypes.c_int64()
     _check(_lib.loom_group_routes_workspace(tokens, routes, experts, ctypes.byref(n)), "group_routes_workspace")
     return n.value
+
+
+_group_need = functools.lru_cache(maxsize=256)(group_routes_workspace)  # a function of the sizes alone
 
 
 def group_routes(ids: torch.Tensor, experts: int, slots: torch.Tensor | None = None, rows: torch.Tensor | None = None,
@@ -582,19 +591,12 @@ def group_routes(ids: torch.Tensor, experts: int, slots: torch.Tensor | None = N
     _dev(ids, torch.int32, "ids", device)
     _require(ids.dim() == 2 and ids.is_contiguous(), "ids must be a contiguous [tokens][routes] tensor")
     tokens, routes = ids.shape
-    need = group_routes_workspace(tokens, routes, experts)
-    if slots is None:
-        slots = torch.empty(tokens, routes, dtype=torch.int32, device=ids.device)
-    _buffer(slots, torch.int32, tokens * routes, "slots", device)
-    if rows is None:
-        rows = torch.empty(tokens * routes, dtype=torch.int32, device=ids.device)
-    _buffer(rows, torch.int32, tokens * routes, "rows", device)
-    if offsets is None:
-        offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
-    _buffer(offsets, torch.int32, experts + 1, "offsets", device)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
-    _buffer(workspace, torch.uint8, need, "workspace", device, optional=need == 0)
+    pairs, need = tokens * routes, _group_need(tokens, routes, experts)
+    slots = _made(slots, torch.int32, (tokens, routes), pairs, "slots", ids, device)
+    rows = _made(rows, torch.int32, pairs, pairs, "rows", ids, device)
+    offsets = _made(offsets, torch.int32, experts + 1, experts + 1, "offsets", ids, device)
+    if workspace is not None or need > 0:
+        workspace = _made(workspace, torch.uint8, need, need, "workspace", ids, device)
     _check(_lib.loom_group_routes(_ptr(ids), tokens, routes, experts, _ptr(slots), _ptr(rows), _ptr(offsets),
                                   _ptr(workspace), need, stream), "group_routes")
     return slots, rows, offsets

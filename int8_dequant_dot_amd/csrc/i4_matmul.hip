@@ -201,7 +201,7 @@ __global__ __launch_bounds__(C::kShape.waves() * kWave, 1) void i4_tile_kernel(I
         loop.rows = (int)min((int64_t)C::TK, p.tokens - loop.t0);
     }
     loop.n0 = (int64_t)ch * C::OUT_CH;
-    const int all = p.chunks / 8, begin = S > 1 ? (int)((int64_t)all * wave / S) : 0;
+    const int all = p.chunks / (4 * C::PARTS), begin = S > 1 ? (int)((int64_t)all * wave / S) : 0;
     const int end = S > 1 ? (int)((int64_t)all * (wave + 1) / S) : all;
     loop.run(begin, end - begin, S == 1 || wave == S - 1, [&](int r) {
         int64_t row = loop.t0 + r;

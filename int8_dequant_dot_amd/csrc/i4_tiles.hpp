@@ -25,28 +25,31 @@ __device__ __forceinline__ void gather_to_lds(const void *from, int at) {
 // l & 31, half h = l >> 5 of the product's 32, and of the sums channel l & 31, tokens
 // 8 (r >> 2) + 4 h + (r & 3).
 //
-// A step is 256 elements of k, two halves of SUBS groups of 128 / SUBS (with one,
-// part of a longer group).  Product i of a half's four takes the 16-element pieces
+// A step is PARTS (1 or 2) parts of 128 elements of k, SUBS groups of 128 / SUBS each
+// (with one, part of a longer group).  Product i of a part's four takes the 16-element pieces
 // piece(i, 0) and piece(i, 1): both halves of 32 neighbours where SUBS is 4, else a
 // half each of two 32s, whose weights are then one read for both.
 //
-// LDS holds two steps: rows of 256 bytes of activations and of 128 bytes of
-// weights, filled by direct loads of whole lines; 16-byte piece c of row r sits at
-// slot c ^ (r & 15) or c ^ (r & 7), so that fragment reads meet no bank twice.
+// LDS holds two steps: rows of 128 PARTS bytes of activations and of 64 PARTS bytes of
+// weights, filled by direct loads; 16-byte piece c of row r sits at slot c ^ swizzle(r),
+// so that fragment reads meet no bank twice.
 template <int SHAPE, int SUBS_, bool GATED_>
 struct I4Tile {
     static constexpr I4TileShape kShape = i4_tile_shape(SHAPE, GATED_);
-    static constexpr int XT = kShape.xt, WN = kShape.wn, WM = kShape.wm, WT = kShape.wt, SUBS = SUBS_;
+    static constexpr int XT = kShape.xt, WN = kShape.wn, WM = kShape.wm, WT = kShape.wt, SUBS = SUBS_, PARTS = kShape.parts;
     static constexpr bool GATED = GATED_;
     static constexpr int NW = WM * WN, TK = kShape.tokens(), CH = kShape.channels(), OUT_CH = GATED ? CH / 2 : CH;
-    static constexpr int kBytesX = TK * 256, kBytesW = CH * 128, kStep = kBytesX + kBytesW;
-    static constexpr int kBytesS = 2 * SUBS * CH * 4;  // a step's scales, as f32
+    static constexpr int kRowX = 128 * PARTS, kRowW = 64 * PARTS, kBytesX = TK * kRowX, kBytesW = CH * kRowW, kStep = kBytesX + kBytesW;
+    static constexpr int kBytesS = PARTS * SUBS * CH * 4;  // a step's scales, as f32
     static constexpr int kLds = 2 * (kStep + kBytesS);
-    static constexpr int XJ = TK / 4 / NW, WJ = CH / 8 / NW;  // direct loads a wave and step
-    static constexpr int SJ = 2 * CH / (NW * kWave);  // channels' halves whose scales a thread loads
-    static constexpr int PER = 4 / SUBS;                      // products of a group within a half
-    static_assert(TK % (4 * NW) == 0 && CH % (8 * NW) == 0 && 2 * CH % (NW * kWave) == 0 && (!GATED || WT == 2), "whole loads a wave");
+    static constexpr int XJ = kBytesX / 1024 / NW, WJ = kBytesW / 1024 / NW;  // direct loads a wave and step
+    static constexpr int SJ = PARTS * CH < NW * kWave ? 1 : PARTS * CH / (NW * kWave);  // channels' parts whose scales a thread loads
+    static constexpr int PER = 4 / SUBS;                      // products of a group within a part
+    static_assert(kBytesX % (1024 * NW) == 0 && kBytesW % (1024 * NW) == 0 && (SJ == 1 || PARTS * CH % (NW * kWave) == 0) &&
+                      (!GATED || WT == 2), "whole loads a wave");
     static_assert(kLds * kShape.split == kShape.lds(SUBS) && kShape.lds(SUBS) <= 160 * 1024, "the launch's LDS");
+    static __device__ constexpr int swizzle_x(int r) { return r & (8 * PARTS - 1); }
+    static __device__ constexpr int swizzle_w(int r) { return PARTS == 2 ? r & 7 : (r >> 1) & 3; }
     static __device__ constexpr int piece(int i, int h) { return SUBS == 4 ? 2 * i + h : 4 * (i >> 1) + 2 * h + (i & 1); }
 };
 
@@ -89,25 +92,25 @@ struct I4TileLoop {
         const char *from_x[C::XJ], *from_w[C::WJ];
 #pragma unroll
         for (int j = 0; j < C::XJ; ++j) {
-            const int r = (wave + C::NW * j) * 4 + (lane >> 4);
-            from_x[j] = (const char *)p.x + row_of(min(r, rows - 1)) * kb + (((lane & 15) ^ (r & 15)) << 4);
+            const int slot = (wave + C::NW * j) * kWave + lane, r = slot / (8 * C::PARTS), c = slot % (8 * C::PARTS);
+            from_x[j] = (const char *)p.x + row_of(min(r, rows - 1)) * kb + ((c ^ C::swizzle_x(r)) << 4);
         }
 #pragma unroll
         for (int j = 0; j < C::WJ; ++j) {
-            const int r = (wave + C::NW * j) * 8 + (lane >> 3);
-            from_w[j] = (const char *)matrix(is_up(r)) + weight_row(r) * (kb / 2) + (((lane & 7) ^ (r & 7)) << 4);
+            const int slot = (wave + C::NW * j) * kWave + lane, r = slot / (4 * C::PARTS), c = slot % (4 * C::PARTS);
+            from_w[j] = (const char *)matrix(is_up(r)) + weight_row(r) * (kb / 2) + ((c ^ C::swizzle_w(r)) << 4);
         }
         const int at = lds_address(lds) + wave * 1024;
         // load J of step s, into that place
         auto load = [&](auto at_j, int64_t s, int place) {
             constexpr int j = decltype(at_j)::value, k = j < C::XJ ? 0 : j - C::XJ;
             const int to = at + (place & 1) * C::kStep;
-            if constexpr (j < C::XJ) gather_to_lds(from_x[j] + (begin + s) * 256, to + C::NW * j * 1024);
-            else gather_to_lds(from_w[k] + (begin + s) * 128, to + C::kBytesX + C::NW * k * 1024);
+            if constexpr (j < C::XJ) gather_to_lds(from_x[j] + (begin + s) * C::kRowX, to + C::NW * j * 1024);
+            else gather_to_lds(from_w[k] + (begin + s) * C::kRowW, to + C::kBytesX + C::NW * k * 1024);
         };
         // Scales: read by every wave that uses them, a line for each lane and two bytes, they
         // took 200 of 1200 us at 4096 x 8192 x 28672.  Each thread reads those of one channel
-        // and half of a step, and they wait in LDS.
+        // and part of a step, and they wait in LDS.
         typedef typename ElementOf<ST>::type Scale;
         typedef Scale Scales __attribute__((ext_vector_type(C::SUBS), aligned(sizeof(Scale))));
         float *const held = (float *)(lds + 2 * C::kStep);
@@ -116,20 +119,20 @@ struct I4TileLoop {
         const int tid = wave * kWave + lane;
 #pragma unroll
         for (int j = 0; j < C::SJ; ++j) {
-            const int r = (tid + j * C::NW * kWave) >> 1;
+            const int r = (tid + j * C::NW * kWave) / C::PARTS % C::CH;
             my_scales[j] = (const Scale *)scales(is_up(r)) + weight_row(r) * p.groups;
         }
         auto fetch_scales = [&](int s) {
             s = begin + min(s, steps - 1);
-            const int h = tid & 1, g = C::SUBS > 1 ? (2 * s + h) * C::SUBS : (8 * s + 4 * h) >> p.chunk_shift;
+            const int h = s * C::PARTS + tid % C::PARTS, g = C::SUBS > 1 ? h * C::SUBS : (4 * h) >> p.chunk_shift;
 #pragma unroll
             for (int j = 0; j < C::SJ; ++j) coming[j] = *(const Scales *)(my_scales[j] + g);
         };
         auto keep_scales = [&](int s) {
 #pragma unroll
             for (int j = 0; j < C::SJ; ++j) {
-                const int r = (tid + j * C::NW * kWave) >> 1;
-                float *to = held + ((s & 1) * 2 + (tid & 1)) * (C::SUBS * C::CH) + r;
+                const int r = (tid + j * C::NW * kWave) / C::PARTS % C::CH;
+                float *to = held + ((s & 1) * C::PARTS + tid % C::PARTS) * (C::SUBS * C::CH) + r;
 #pragma unroll
                 for (int u = 0; u < C::SUBS; ++u) to[u * C::CH] = (float)coming[j][u];
             }
@@ -145,10 +148,11 @@ struct I4TileLoop {
             meet();
             constexpr int WL = C::SUBS == 4 ? 4 : 2;
             int4v a[4], raw[C::WT][WL], b[C::WT][4];
-            const char *base_x = lds + (wn * C::XT * 32 + m) * 256, *base_w = lds + C::kBytesX + (wm * C::WT * 32 + m) * 128;
-            // fragments of half h (0, 1) of the step at that place
+            const char *base_x = lds + (wn * C::XT * 32 + m) * C::kRowX;
+            const char *base_w = lds + C::kBytesX + (wm * C::WT * 32 + m) * C::kRowW;
+            // fragments of part h of the step at that place
             auto read_a = [&](int place, int h, int x, int i) {
-                a[i] = *(const int4v *)(base_x + place + x * 8192 + (((8 * h + C::piece(i, half)) ^ (m & 15)) << 4));
+                a[i] = *(const int4v *)(base_x + place + x * 32 * C::kRowX + (((8 * h + C::piece(i, half)) ^ C::swizzle_x(m)) << 4));
             };
             auto read_w = [&](int place, int h) {
 #pragma unroll
@@ -156,7 +160,7 @@ struct I4TileLoop {
 #pragma unroll
                     for (int i = 0; i < WL; ++i) {
                         const int c = 4 * h + (C::SUBS == 4 ? i : 2 * i + half);
-                        raw[w][i] = *(const int4v *)(base_w + place + w * 4096 + ((c ^ (m & 7)) << 4));
+                        raw[w][i] = *(const int4v *)(base_w + place + w * 32 * C::kRowW + ((c ^ C::swizzle_w(m)) << 4));
                     }
             };
             auto unpack = [&](int w, int i) {
@@ -176,15 +180,16 @@ struct I4TileLoop {
                 const int place = (s & 1) * C::kStep, other = C::kStep - place;
                 const int64_t after = min(s + 2, steps - 1);  // past the end the last step again
                 fetch_scales(s + 1);
-                const float *my = held + (s & 1) * (2 * C::SUBS * C::CH) + wm * C::WT * 32 + m;
+                const float *my = held + (s & 1) * (C::PARTS * C::SUBS * C::CH) + wm * C::WT * 32 + m;
                 // units of PER products that end a group's part, block by block; while one is
                 // multiplied the sums of the one before are converted, scaled and added, and in
-                // the last blocks the next half's fragments are read and unpacked into the
+                // the last blocks the next part's fragments are read and unpacked into the
                 // registers that the products leave
                 constexpr int UNITS = C::XT * C::WT * C::SUBS;
-                each_index<2>([&](auto at_h) {
-                    constexpr int h = decltype(at_h)::value;
-                    const int then = h == 0 ? place : other;
+                each_index<C::PARTS>([&](auto at_h) {
+                    constexpr int h = decltype(at_h)::value, then_h = (h + 1) % C::PARTS;
+                    constexpr bool last = h == C::PARTS - 1;
+                    const int then = last ? other : place;
 #pragma unroll
                     for (int w = 0; w < C::WT; ++w)
 #pragma unroll
@@ -195,7 +200,7 @@ struct I4TileLoop {
                         each_index<C::PER>([&](auto at_i) {
                             constexpr int i = decltype(at_i)::value, q = sub * C::PER + i;
                             if constexpr (x == C::XT - 1 && w == 0 && q == 0) {
-                                if constexpr (h == 1) {
+                                if constexpr (last) {
                                     // all fragments of this step are in registers, and this wave's part
                                     // of the next step is in LDS: once every wave is here the next step
                                     // may be read and this one's place filled
@@ -204,19 +209,19 @@ struct I4TileLoop {
                                     wait_lds();
                                     meet();
                                 }
-                                read_w(then, 1 - h);
+                                read_w(then, then_h);
                             }
                             if constexpr (u < UNITS)
                                 sum[u & 1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[q], b[w][q], i == 0 ? int16v{} : sum[u & 1], 0, 0, 0);
                             if constexpr (u < UNITS && w == C::WT - 1) {
                                 if constexpr (x + 1 < C::XT) read_a(place, h, x + 1, q);
-                                else read_a(then, 1 - h, 0, q);
+                                else read_a(then, then_h, 0, q);
                             }
                             if constexpr (u < UNITS && x == C::XT - 1 && w == C::WT - 1) {
 #pragma unroll
                                 for (int y = 0; y < C::WT; ++y) unpack(y, q);
                             }
-                            if constexpr (h == 1 && u < UNITS && x == C::XT - 1) {
+                            if constexpr (last && u < UNITS && x == C::XT - 1) {
                                 constexpr int n = w * 4 + q, J = C::XJ + C::WJ;
                                 each_index<J>([&](auto at_j) {
                                     if constexpr (decltype(at_j)::value * 4 * C::WT / J == n) load(at_j, after, s);
@@ -235,9 +240,9 @@ struct I4TileLoop {
             }
             wait_loads<0>();
         }
-        // the rest of k, up to seven times 32 elements, in parts of a group and at most 128
+        // the rest of k, less than a step, in parts of a group and at most 128
         constexpr int kPart = 4 / C::SUBS;
-        for (int c0 = tail ? p.chunks / 8 * 8 : p.chunks; c0 < p.chunks; c0 += kPart) {
+        for (int c0 = tail ? p.chunks / (4 * C::PARTS) * (4 * C::PARTS) : p.chunks; c0 < p.chunks; c0 += kPart) {
             const int c1 = min(c0 + kPart, p.chunks), g = c0 >> p.chunk_shift;
 #pragma unroll
             for (int x = 0; x < C::XT; ++x) {

@@ -678,17 +678,17 @@ constexpr int i4_stream_slots(int64_t tokens, int64_t experts, int subs) {
 // Tiles of the 4-bit products: xt x wt blocks of 32 tokens x 32 channels a wave, wn x wm
 // waves, or `split` waves that share a block and split k.
 struct I4TileShape {
-    int xt, wn, wm, wt, split;
+    int xt, wn, wm, wt, split, parts;  // parts: 128s of k in a step
     double step_us[3], work_us[3];  // for 1, 2 and 4 groups in 128
     constexpr int tokens() const { return 32 * xt * wn; }
     constexpr int channels() const { return 32 * wm * wt; }
     constexpr int waves() const { return wn * wm * split; }
-    constexpr int lds(int subs) const { return 2 * split * (tokens() * 256 + channels() * (128 + 8 * subs)); }
+    constexpr int lds(int subs) const { return 2 * split * parts * (tokens() * 128 + channels() * (64 + 4 * subs)); }
 };
 constexpr int kI4TileCount = 4;
 constexpr I4TileShape kI4Tiles[kI4TileCount] = {
-    {2, 2, 4, 2, 1, {2.3, 2.6, 4.4}, {2.3, 2.6, 4.4}}, {1, 2, 2, 2, 1, {1.2, 1.4, 2.4}, {0.9, 1.1, 1.6}},
-    {1, 1, 4, 1, 1, {0.85, 1.0, 1.4}, {0.5, 0.6, 0.9}}, {1, 1, 1, 1, 4, {1.2, 1.4, 1.7}, {1.2, 1.4, 1.7}}};
+    {2, 2, 4, 2, 1, 2, {2.3, 2.6, 4.4}, {2.3, 2.6, 4.4}}, {1, 2, 2, 2, 1, 2, {1.2, 1.4, 2.4}, {0.9, 1.1, 1.6}},
+    {1, 1, 4, 1, 1, 2, {0.85, 1.0, 1.4}, {0.5, 0.6, 0.9}}, {1, 1, 1, 1, 8, 1, {0.8, 0.9, 1.1}, {0.8, 0.9, 1.1}}};
 // A gated wave has a block of either projection.
 constexpr I4TileShape i4_tile_shape(int shape, bool gated) {
     I4TileShape t = kI4Tiles[shape];
@@ -702,7 +702,7 @@ constexpr int64_t i4_tile_rows(int64_t tokens, int64_t experts, int size) {  // 
     return experts > 0 ? tokens / size + (tokens < experts ? tokens : experts) : ceil_of(tokens, size);
 }
 // The tile shape (an index of kI4Tiles) with the least estimated time: a round of r
-// workgroups a CU takes, for each step of 256, the shape's latency or r times its work
+// workgroups a CU takes, for each step, the shape's latency or r times its work
 // (us, measured), whichever is longer; the launch its rounds, or the memory's time for
 // the weights at 6 TB/s.  Routed tiles are counted as if each expert's last were half
 // full, and take longer, since few of them share weights; gated waves of the last
@@ -727,7 +727,7 @@ constexpr int i4_tile_choice(int64_t rows, int64_t k, int64_t tokens, int64_t ex
             const double r = last ? (double)rest : (double)resident, times = last ? (rest > 0) : (double)full;
             const double work = r * t.work_us[at] * slower;
             const double step = work > t.step_us[at] * slower ? work : t.step_us[at] * slower;
-            us += times * (step * (double)k / (256 * t.split) + 3);
+            us += times * (step * (double)k / (128 * t.parts * t.split) + 3);
         }
         const double memory = (double)(experts > 0 ? live : 1) * (double)rows * (gated ? 2 : 1) * (double)k / 12e6;
         if (memory > us) us = memory + 0.1 * us;
