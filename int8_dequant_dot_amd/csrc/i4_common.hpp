@@ -40,6 +40,8 @@ __device__ __forceinline__ int wave_scan(int v) {
 // or out of range make an expert's rows fewer, never others.
 __device__ __forceinline__ bool routed_tile(const I4Product &p, int size, int64_t index, int &expert, int64_t &first, int &rows) {
     const int lane = lane_id();
+    // more tiles than a grid has, so that sums stay in 32 bits whatever the offsets say
+    constexpr int64_t kMost = 1 << 24;
     int64_t before = 0;
     for (int e0 = 0; e0 < p.experts; e0 += kWave) {
         const int e = e0 + lane;
@@ -48,7 +50,7 @@ __device__ __forceinline__ bool routed_tile(const I4Product &p, int size, int64_
             begin = max(p.offsets[e], 0);
             end = min(p.offsets[e + 1], p.tokens);
         }
-        const int n = end > begin ? end - begin : 0, tiles = (int)(((int64_t)n + size - 1) / size);
+        const int n = end > begin ? end - begin : 0, tiles = (int)min(((int64_t)n + size - 1) / size, kMost);
         const int scan = wave_scan(tiles);
         const uint64_t past = __ballot(before + scan > index);
         if (past) {

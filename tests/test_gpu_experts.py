@@ -570,6 +570,68 @@ def test_experts_bad_offsets_and_index(loom, device):
     assert torch.equal(out.cpu().isnan().all(1), bad) and torch.equal(out.cpu().isnan().any(1), bad)
 
 
+def test_offsets_that_overlap(loom, device):
+    """Every expert claims every row, 1024 times: rows with several claims have no defined value, the others stay."""
+    experts, rows, k, pairs = 1024, 16, 64, 300
+    s = operands(experts, rows, k, pairs, 64, F32, 2)
+    d = {m: t.to(device) for m, t in s.items()}
+    offsets = torch.tensor([0, 2 ** 31 - 1] * 512 + [0], dtype=torch.int32, device=device)
+    for n in (1, 20, pairs):
+        out = torch.full((pairs + 8, rows), 7.0, device=device)
+        loom.i4_expert_matmul(loom.pack_int4(d["w"]), d["ws"], loom.pack_int8(d["x"][:n]), d["xs"], offsets, group=64, out=out[:n])
+        assert bool((out[n:] == 7).all())
+
+
+@pytest.mark.parametrize("pairs", [3, 700])
+def test_weights_and_rows_past_32_bits(loom, device, pairs):
+    """Weights of 5.4 GB and activations of 4.6 GB, of which the far ends are used."""
+    experts, rows, k = 40, 8192, 32768
+    words = torch.zeros(experts, rows, k // 8, dtype=torch.int32, device=device)
+    scale = torch.ones(experts, rows, k // 256, dtype=F16, device=device)
+    x_rows = 141000
+    x = torch.zeros(x_rows, k // 4, dtype=torch.int32, device=device)
+    g = torch.Generator().manual_seed(pairs)
+    wq = torch.randint(-8, 8, (32, k), generator=g, dtype=torch.int8)
+    xq = torch.randint(-128, 128, (4, k), generator=g, dtype=torch.int8)
+    words[-1, -32:] = loom.pack_int4(wq.to(device))
+    x[-4:] = loom.pack_int8(xq.to(device))
+    index = torch.randint(x_rows - 4, x_rows, (pairs,), generator=g, dtype=torch.int32)
+    offsets = torch.zeros(experts + 1, dtype=torch.int32, device=device)
+    offsets[-1] = pairs
+    out = loom.i4_expert_matmul(words, scale, x, None, offsets, index=index.to(device), group=256, dtype=F32).cpu()
+    want = xq.double() @ wq.double().t()
+    # whole numbers whose sums stay below 2^24
+    assert torch.equal(out[:, -32:].double(), want[(index - (x_rows - 4)).long()]) and bool((out[:, :-32] == 0).all())
+
+
+def test_output_past_2_31_elements(loom, device):
+    rows, k, tokens = 32768, 32, 66000
+    g = torch.Generator().manual_seed(1)
+    wq = torch.randint(-8, 8, (rows, k), generator=g, dtype=torch.int8)
+    xq = torch.randint(-128, 128, (tokens, k), generator=g, dtype=torch.int8)
+    out = loom.i4_matmul(loom.pack_int4(wq.to(device)), torch.ones(rows, 1, device=device), loom.pack_int8(xq.to(device)), group=32,
+                         dtype=F16)
+    for at in (0, 40000, 65535, 65536, tokens - 1):
+        assert torch.equal(out[at].cpu().double(), (wq.double() @ xq[at].double()).half().double())
+
+
+def test_same_bits_every_time(loom, device):
+    """No result depends on which wave comes first."""
+    s = operands(6, 96, 2080, 400, 32, F16, 3, ("w", "u"))
+    d = {m: t.to(device) for m, t in s.items()}
+    w, u, x = loom.pack_int4(d["w"]), loom.pack_int4(d["u"]), loom.pack_int8(d["x"])
+    logits = torch.randn(3000, 96, device=device)
+    for n in (1, 6, 30, 400):
+        off = offsets_of([n // 3, 0, n // 2, 0, 0, n - n // 3 - n // 2]).to(device)
+        runs = [(loom.i4_matmul(w[0], d["ws"][0], x[:n], d["xs"], group=32, dtype=F32),
+                 loom.i4_expert_gated_projection(w, d["ws"], u, d["us"], x[:n], d["xs"], off, group=32, dtype=F32))
+                for _ in range(4)]
+        assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(runs[0], r))
+    runs = [(*loom.route_experts(logits, 5, "sigmoid", logits[0] * 0.1, 8, 4), *loom.group_routes(loom.route_experts(logits, 5)[0], 96))
+            for _ in range(4)]
+    assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(runs[0], r))
+
+
 # ------------------------------------------------------------------ together
 
 class Layer:
