@@ -26,6 +26,12 @@ namespace {
 // A segment of 128 is a group, or a part of one.  Of shorter groups it holds SUB = 2 or
 // 4: a token then takes SUB slots, each of which sees the quarters l >> 4 of its own
 // group and zeros elsewhere.
+//
+// Memory bounds it: one token x 16384 x 8192 in groups of 128 takes 13.1 us (5.3 TB/s, of
+// it about 2.4 us a launch), the gated rows of 32 tokens x 8 routes over 128 experts of
+// 2048 x 4096 168 us (6.6 TB/s).  A workgroup of 16 rows took 14.8 and 250 us, three
+// records in flight 16.7 and 310, eight waves 18.7 and 257; 64-bit addresses instead of
+// offsets from the tile 13.7 and 222.
 template <int ST, int RI, int VG>
 struct I4Record {
     int4v w[RI], x[VG][2];
@@ -177,10 +183,12 @@ __global__ __launch_bounds__(kWave * kI4StreamWaves, 2) void i4_stream_kernel(I4
     }
 }
 
-// Several split waves (of one wave's tile each) share a tile: each takes a run of k over
+// Two waves a SIMD are asked for where the shape has them: the compiler then leaves the
+// products' sums in vector registers, where they are converted (5 to 8 % of a tile of four
+// waves).  Several split waves (of one wave's tile each) share a tile: each takes a run of k over
 // LDS of its own, with no barrier, and the sums are added in their order at the end.
 template <bool ROUTED, typename C, int ST>
-__global__ __launch_bounds__(C::kShape.waves() * kWave, 1) void i4_tile_kernel(I4Product p, int type) {
+__global__ __launch_bounds__(C::kShape.waves() * kWave, C::kShape.waves() >= 4 ? 2 : 1) void i4_tile_kernel(I4Product p, int type) {
     constexpr int S = C::kShape.split;
     static_assert(S == 1 || (C::NW == 1 && C::kLds >= C::XT * C::WT * 4096), "the sums fit the steps");
     __shared__ __align__(1024) char lds[S * C::kLds];

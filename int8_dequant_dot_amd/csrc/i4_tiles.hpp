@@ -33,6 +33,16 @@ __device__ __forceinline__ void gather_to_lds(const void *from, int at) {
 // LDS holds two steps: rows of 128 PARTS bytes of activations and of 64 PARTS bytes of
 // weights, filled by direct loads; 16-byte piece c of row r sits at slot c ^ swizzle(r),
 // so that fragment reads meet no bank twice.
+//
+// What bounds it is the vector unit: each sum of 32 x 32 x 128 takes a conversion and a
+// multiply-add (256 of the 530 vector instructions of a wave's step of 256), its weights
+// three instructions for two registers.  4096 tokens x 8192 channels x k 28672 takes 1.05 ms
+// in groups of 128 (1840 TOP/s; without loads 0.88 to 0.93), 1.95 ms in groups of 32, four
+// times the conversions.  Not kept at that size: weights straight from memory to registers
+// (1.64 ms: a line for every 16 bytes of a lane), reads that wait for the barrier of their
+// own step (1.24 ms), scales read by each lane (1.21 ms), one wave a SIMD with twice the
+// tokens (1.22 ms: the sums go through the accumulation registers), 128 x 128 tiles, two a
+// CU (1.17 ms).
 template <int SHAPE, int SUBS_, bool GATED_>
 struct I4Tile {
     static constexpr I4TileShape kShape = i4_tile_shape(SHAPE, GATED_);
@@ -109,7 +119,7 @@ struct I4TileLoop {
             else gather_to_lds(from_w[k] + (begin + s) * C::kRowW, to + C::kBytesX + C::NW * k * 1024);
         };
         // Scales: read by every wave that uses them, a line for each lane and two bytes, they
-        // took 200 of 1200 us at 4096 x 8192 x 28672.  Each thread reads those of one channel
+        // took 110 of 1200 us at 4096 x 8192 x 28672.  Each thread reads those of one channel
         // and part of a step, and they wait in LDS.
         typedef typename ElementOf<ST>::type Scale;
         typedef Scale Scales __attribute__((ext_vector_type(C::SUBS), aligned(sizeof(Scale))));

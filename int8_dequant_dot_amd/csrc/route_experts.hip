@@ -10,6 +10,13 @@
 // order is that of its 64-bit value: waves whose f32 choices lie apart by more
 // than their error are done with those, the few others compute them again in 64
 // bits.  Weights are f32.
+//
+// The vector unit bounds it: 65536 tokens x 256 experts in f32, the 8 best of 4 of 8
+// groups by sigmoid and bias, take 54 to 60 us, where their 71 MB would take 15; a wave
+// of four tokens runs 1.4 thousand instructions.  16 lanes hold a token where there are
+// many (fewer cross-lane steps a token), 64 where there are few.  With every choice in 64
+// bits the same took 190 us.
+// The gradient streams: 65536 x 256 bfloat16 logits through the softmax take 19 us (3.7 TB/s).
 #include <type_traits>
 
 #include "ffn_common.hpp"
@@ -162,7 +169,7 @@ __device__ __forceinline__ void merge_two(int &first, int &second) {
 // choice, or the sum of its two largest, and a group stays while fewer than top_groups
 // are better.  margin: how far the worst of those that stay lies above the best of
 // the others (groups without a choice apart: it does not matter whether they stay).
-// room: LDS of this token, experts + groups values.
+// room: LDS of this token, experts + 2 groups values.
 template <int LOG, int R>
 __device__ __forceinline__ void best_groups(const RouteArgs &a, int sub, float *room, int (&c)[R], float &margin) {
     typedef Held<LOG, R> H;
@@ -182,7 +189,7 @@ __device__ __forceinline__ void best_groups(const RouteArgs &a, int sub, float *
     if (H::V == 4 && size >= 4 && size <= 4 * L && (size & (size - 1)) == 0) {
         // groups of 4, 8, .. neighbouring experts lie on 1, 2, .. neighbouring lanes
         const int shift = __builtin_ctz(size);
-        int mine[B], group[B], better[B] = {};
+        int group[B];
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             int first = kNone, second = kNone;
@@ -197,21 +204,23 @@ __device__ __forceinline__ void best_groups(const RouteArgs &a, int sub, float *
                 case 7: merge_two<(LOG >= 5 ? 5 : 0)>(first, second); break;
                 default: merge_two<(LOG >= 6 ? 6 : 0)>(first, second);
             }
-            mine[b] = value(first, second);
             const int e = H::expert_at(4 * b, sub);
             group[b] = e >> shift;
-            if (e < a.experts && (e & (size - 1)) == 0) ranks[group[b]] = mine[b];
+            if (e < a.experts && (e & (size - 1)) == 0) ranks[group[b]] = value(first, second);
         }
         wave_fence();
-        for (int o = 0; o < a.groups; ++o) {
-            const int that = ranks[o];
-#pragma unroll
-            for (int b = 0; b < B; ++b) better[b] += that - (o >= group[b]) >= mine[b];  // equal and before it, or greater
+        // a lane a group: how many are better (equal and before it, or greater)
+        for (int g = sub; g < a.groups; g += L) {
+            const int that = ranks[g];
+            int better = 0;
+            for (int o = 0; o < a.groups; ++o) better += ranks[o] - (o >= g) >= that;
+            weigh(better < a.top_groups, that);
+            ranks[a.groups + g] = better;
         }
+        wave_fence();
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-            const bool stays = better[b] < a.top_groups;
-            weigh(stays, mine[b]);
+            const bool stays = ranks[a.groups + min(group[b], a.groups - 1)] < a.top_groups;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (4 * b + i < R) c[4 * b + i] = stays ? c[4 * b + i] : kNone;
@@ -325,7 +334,7 @@ struct SortedChoice {
     __device__ __forceinline__ SortedChoice(const int (&key)[R], int sub, int *room_) : room(room_) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            h[r] = key[r] == kNone ? kNone : (key[r] & ~LOW) | (LOW - (EXACT ? H::expert_at(r, sub) : r));
+            h[r] = (key[r] & ~LOW) | (LOW - (EXACT ? H::expert_at(r, sub) : r));  // none: kNone or less
         sort_heads(h);
         room[sub] = kNone;
         wave_fence();
