@@ -671,6 +671,7 @@ constexpr int kI4StreamWaves = 4, kI4StreamLoads = 8;
 // rows each, 64 experts x 2048 x 2048 took 50 us so and 33 us in tiles, while at 28672 x
 // 8192, dense, 6 tokens took 26 us so and 38 us in tiles.
 constexpr int i4_stream_slots(int64_t tokens, int64_t experts, int subs) {
+    if (tokens == 0) return 4;
     const int64_t each = experts > 0 ? ceil_of(tokens, tokens < experts ? tokens : experts) : tokens;
     return each * subs <= 4 ? 4 : experts == 0 && each * subs <= 8 ? 8 : 0;
 }

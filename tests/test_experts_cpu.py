@@ -170,6 +170,15 @@ def test_launch_geometry(loom, name, load):
                             fits([rows, k, tokens, group] + ([experts] if name != "i4_matmul" else []))
 
 
+@pytest.mark.parametrize("name", ["i4_matmul", "i4_expert_matmul", "i4_expert_gated_projection"])
+def test_nothing_to_do_has_no_grid(loom, name):
+    token = loom.launch_config_lookup(name)
+    for rows, k, tokens in ((64, 128, 0), (0, 128, 5), (0, 0, 0)):
+        for group in (32, 128):
+            work = [rows, k, tokens, group] + ([] if name == "i4_matmul" else [8])
+            assert loom.launch_config_invoke(token, work)["workgroups"][0] == 0
+
+
 def test_pack_int4(loom):
     g = torch.Generator().manual_seed(0)
     for shape in ((1, 32), (3, 96), (2, 5, 64), (4, 0), (0, 64)):

@@ -615,6 +615,22 @@ def test_output_past_2_31_elements(loom, device):
         assert torch.equal(out[at].cpu().double(), (wq.double() @ xq[at].double()).half().double())
 
 
+def test_nothing_routed(loom, device):
+    """No tokens, and tokens without a single route."""
+    s = operands(4, 40, 64, 3, 32, F32, 1)
+    w, ws, x = loom.pack_int4(s["w"].to(device)), s["ws"].to(device), loom.pack_int8(s["x"].to(device))
+    none = torch.zeros(5, dtype=torch.int32, device=device)
+    assert loom.i4_expert_matmul(w, ws, x[:0], None, none, group=32).shape == (0, 40)
+    assert loom.i4_expert_gated_projection(w, ws, w, ws, x[:0], None, none, group=32).shape == (0, 40)
+    assert loom.i4_matmul(w[0], ws[0], x[:0], group=32).shape == (0, 40)
+    out = torch.full((3, 40), 7.0, device=device)
+    loom.i4_expert_gated_projection(w, ws, w, ws, x, None, none, group=32, out=out)
+    assert bool((out == 7).all())
+    ids = torch.full((3, 2), -1, dtype=torch.int32, device=device)
+    slots, rows, offsets = loom.group_routes(ids, 4)
+    assert bool((slots == -1).all()) and bool((rows == -1).all()) and bool((offsets == 0).all())
+
+
 def test_same_bits_every_time(loom, device):
     """No result depends on which wave comes first."""
     s = operands(6, 96, 2080, 400, 32, F16, 3, ("w", "u"))
