@@ -25,6 +25,16 @@ namespace loom {
 
 namespace {
 
+// body(0) .. body(N - 1), each index a constant from the start: arrays that are
+// written under conditions in unrolled loops have ended in scratch memory.
+template <int N, int I = 0, typename Body>
+__device__ __forceinline__ void each(Body &&body) {
+    if constexpr (I < N) {
+        body(std::integral_constant<int, I>{});
+        each<N, I + 1>(body);
+    }
+}
+
 // ---------------------------------------------------------------- within the lanes of a token
 // Step S of a butterfly over aligned groups of 2^LOG lanes: the value of the
 // lane (or of a lane with the same partial result) on the other side.
@@ -218,13 +228,16 @@ __device__ __forceinline__ void best_groups(const RouteArgs &a, int sub, float *
             ranks[a.groups + g] = better;
         }
         wave_fence();
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
+        each<B>([&](auto b) {
             const bool stays = ranks[a.groups + min(group[b], a.groups - 1)] < a.top_groups;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (4 * b + i < R) c[4 * b + i] = stays ? c[4 * b + i] : kNone;
-        }
+            each<4>([&](auto i) {
+                constexpr int r = 4 * decltype(b)::value + decltype(i)::value;
+                if constexpr (r < R) {
+                    const int own = c[r];
+                    c[r] = stays ? own : kNone;
+                }
+            });
+        });
     } else {
         int *const values = (int *)room;
 #pragma unroll
@@ -287,29 +300,30 @@ __device__ __forceinline__ void order(int &a, int &b) {
     a = max(a, b);
     b = low;
 }
-__device__ __forceinline__ void sort8(int *h) {
-    order(h[0], h[1]), order(h[2], h[3]), order(h[4], h[5]), order(h[6], h[7]);
-    order(h[0], h[2]), order(h[1], h[3]), order(h[4], h[6]), order(h[5], h[7]);
-    order(h[1], h[2]), order(h[5], h[6]);
-    order(h[0], h[4]), order(h[1], h[5]), order(h[2], h[6]), order(h[3], h[7]);
-    order(h[2], h[4]), order(h[3], h[5]);
-    order(h[1], h[2]), order(h[3], h[4]), order(h[5], h[6]);
+template <int O, int R>
+__device__ __forceinline__ void sort8(int (&h)[R]) {
+    order(h[O], h[O + 1]), order(h[O + 2], h[O + 3]), order(h[O + 4], h[O + 5]), order(h[O + 6], h[O + 7]);
+    order(h[O], h[O + 2]), order(h[O + 1], h[O + 3]), order(h[O + 4], h[O + 6]), order(h[O + 5], h[O + 7]);
+    order(h[O + 1], h[O + 2]), order(h[O + 5], h[O + 6]);
+    order(h[O], h[O + 4]), order(h[O + 1], h[O + 5]), order(h[O + 2], h[O + 6]), order(h[O + 3], h[O + 7]);
+    order(h[O + 2], h[O + 4]), order(h[O + 3], h[O + 5]);
+    order(h[O + 1], h[O + 2]), order(h[O + 3], h[O + 4]), order(h[O + 5], h[O + 6]);
 }
 template <int R>
 __device__ __forceinline__ void sort_heads(int (&k)[R]) {
     if constexpr (R == 4) {
         order(k[0], k[1]), order(k[2], k[3]), order(k[0], k[2]), order(k[1], k[3]), order(k[1], k[2]);
     } else if constexpr (R >= 8) {
-        sort8(k);
+        sort8<0>(k);
         if constexpr (R == 16) {
-            sort8(k + 8);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) k[i] = max(k[i], k[15 - i]);
-#pragma unroll
-            for (int d = 4; d > 0; d /= 2)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (!(i & d)) order(k[i], k[i + d]);
+            sort8<8>(k);
+            each<8>([&](auto i) { k[i] = max(k[i], k[15 - i]); });
+            each<3>([&](auto s) {
+                constexpr int d = 4 >> decltype(s)::value;
+                each<8>([&](auto i) {
+                    if constexpr (!(decltype(i)::value & d)) order(k[i], k[i + d]);
+                });
+            });
         }
     }
 }
@@ -327,21 +341,20 @@ template <bool EXACT, int LOG, int R>
 struct SortedChoice {
     typedef Held<LOG, R> H;
     static constexpr int D = R < 8 ? R : 8, LOW = EXACT ? H::L * R - 1 : R - 1;
-    int h[R], popped = 0, taken = 0;
-    bool lost = false;
-    int *const room;
 
-    __device__ __forceinline__ SortedChoice(const int (&key)[R], int sub, int *room_) : room(room_) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            h[r] = (key[r] & ~LOW) | (LOW - (EXACT ? H::expert_at(r, sub) : r));  // none: kNone or less
+    // Turns keys into this lane's list.
+    static __device__ __forceinline__ void sort(int (&h)[R], int sub, int *room) {
+        each<R>([&](auto r) {  // none: kNone or less
+            h[r] = (h[r] & ~LOW) | (LOW - (EXACT ? H::expert_at(r, sub) : (int)r));
+        });
         sort_heads(h);
         room[sub] = kNone;
         wave_fence();
     }
-    // Writes down choices up to `count`, at most L.
-    __device__ __forceinline__ void take(int count, int sub) {
-        for (; taken < count; ++taken) {
+    // Writes down the choices from..count - 1, count at most L; popped: how many were this lane's.
+    static __device__ __forceinline__ bool take(int (&h)[R], int &popped, int from, int count, int sub, int *room) {
+        bool lost = false;
+        for (int taken = from; taken < count; ++taken) {
             const int best = fold_max<LOG>(h[0]);
             const bool some = best > kNone, hit = some && h[0] == best;
             if (hit) {
@@ -352,27 +365,29 @@ struct SortedChoice {
                 const uint64_t hits = __builtin_amdgcn_ballot_w64(hit), lanes = __builtin_amdgcn_ballot_w64(some);
                 if (__builtin_popcountll(hits) != __builtin_popcountll(lanes) >> LOG) lost = true;  // two alike
             }
-#pragma unroll
-            for (int i = 0; i < D; ++i) h[i] = hit ? (i + 1 < D ? h[i + 1] : kNone) : h[i];
+            each<D>([&](auto i) {
+                int next = kNone;
+                if constexpr (decltype(i)::value + 1 < D) next = h[decltype(i)::value + 1];
+                const int own = h[i];
+                h[i] = hit ? next : own;
+            });
             popped += hit;
         }
-        if (D < R && popped >= D) lost = true;  // this lane's list is used up, its keys may not be
         wave_fence();
+        return lost || (D < R && popped >= D);  // this lane's list is used up, its keys may not be
     }
-    __device__ __forceinline__ float value(int i) const { return of_key(room[i] & ~LOW); }
-    __device__ __forceinline__ bool some(int i) const { return room[i] > kNone; }
+    static __device__ __forceinline__ float value(const int *room, int i) { return of_key(room[i] & ~LOW); }
     static __device__ __forceinline__ bool apart(float high, float low, float gap) {
         return high - low > gap + 0x1p-19f * (fabsf(high) + fabsf(low));
     }
     // Whether the choice after lane sub's lies apart from it, or there is none.
-    __device__ __forceinline__ bool clear(int sub, float gap) const {
-        return sub + 1 >= taken || !some(sub + 1) || apart(value(sub), value(sub + 1), gap);
+    static __device__ __forceinline__ bool clear(const int *room, int taken, int sub, float gap) {
+        return sub + 1 >= taken || room[sub + 1] <= kNone || apart(value(room, sub), value(room, sub + 1), gap);
     }
     // Lane sub's choice, -1 where there is none.
-    __device__ __forceinline__ int expert(int sub) const {
+    static __device__ __forceinline__ int expert(const int *room, int taken, int sub) {
         const int best = room[sub], low = LOW - (best & LOW);
-        const int id = sub < taken && best > kNone ? (EXACT ? low : H::expert_at(low, room[H::L + sub])) : -1;
-        return id;
+        return sub < taken && best > kNone ? (EXACT ? low : H::expert_at(low, room[H::L + sub])) : -1;
     }
 };
 
@@ -483,18 +498,21 @@ __device__ __forceinline__ int choose_wide(const RouteArgs &a, int sub, float to
 // room for the choice behind the last.)
 template <int LOG, int R>
 __device__ __forceinline__ int largest_logits(const RouteArgs &a, int sub, int bad, int (&c)[R], int *room) {
-    int id;
+    int id, h[R], popped = 0;
     bool sure;
+    each<R>([&](auto r) { h[r] = c[r]; });
     if (a.type == LOOM_F32) {
-        SortedChoice<false, LOG, R> sorted(c, sub, room);
-        sorted.take(min(a.top_k + 1, 1 << LOG), sub);
-        id = sorted.expert(sub);
-        sure = !sorted.lost && a.top_k < 1 << LOG && sorted.clear(sub, 0.0f);
+        typedef SortedChoice<false, LOG, R> Sorted;
+        const int taken = min(a.top_k + 1, 1 << LOG);
+        Sorted::sort(h, sub, room);
+        const bool lost = Sorted::take(h, popped, 0, taken, sub, room);
+        id = Sorted::expert(room, taken, sub);
+        sure = !lost && a.top_k < 1 << LOG && Sorted::clear(room, taken, sub, 0.0f);
     } else {
-        SortedChoice<true, LOG, R> sorted(c, sub, room);
-        sorted.take(a.top_k, sub);
-        id = sorted.expert(sub);
-        sure = !sorted.lost;
+        typedef SortedChoice<true, LOG, R> Sorted;
+        Sorted::sort(h, sub, room);
+        sure = !Sorted::take(h, popped, 0, a.top_k, sub, room);
+        id = Sorted::expert(room, a.top_k, sub);
     }
     wave_fence();
     if (__ballot(!sure && !bad)) id = largest<LOG, R>(a.top_k, sub, c);
@@ -502,7 +520,7 @@ __device__ __forceinline__ int largest_logits(const RouteArgs &a, int sub, int b
 }
 
 template <int LOG, int R>
-__global__ __launch_bounds__(kRouteWaves * kWave, R < 16 ? 4 : 3) void route_kernel(RouteArgs given) {
+__global__ __launch_bounds__(kRouteWaves * kWave, R == 16 ? (LOG == 4 ? 3 : 2) : 4) void route_kernel(RouteArgs given) {
     RouteArgs a = given;
     typedef Held<LOG, R> H;
     constexpr int L = H::L, PER = kRouteWaves * kWave / L;  // tokens of a workgroup
@@ -566,11 +584,12 @@ __global__ __launch_bounds__(kRouteWaves * kWave, R < 16 ? 4 : 3) void route_ker
             const float unit = 1.0f / total;  // a softmax's largest score
             const float gap = (sigmoid ? 0x1p-21f : unit * 0x1p-17f) + largest_bias * 0x1p-23f;
             int choice[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float score = sigmoid ? loom::sigmoid(l[r]) : s[r] * unit;
-                choice[r] = l[r] == -kInf ? kNone : key_of(score + bias[r]);
-            }
+            if (sigmoid) each<R>([&](auto r) { s[r] = loom::sigmoid(l[r]); });
+            else each<R>([&](auto r) { s[r] = s[r] * unit; });
+            each<R>([&](auto r) {
+                const int key = key_of(s[r] + bias[r]);
+                choice[r] = l[r] == -kInf ? kNone : key;
+            });
             bool sure = true;
             if (a.groups > 1) {
                 best_groups<LOG, R>(a, sub, (float *)room, choice, margin);
@@ -578,18 +597,20 @@ __global__ __launch_bounds__(kRouteWaves * kWave, R < 16 ? 4 : 3) void route_ker
             }
             if (a.bias) {
                 typedef SortedChoice<false, LOG, R> Sorted;
-                Sorted sorted(choice, sub, (int *)room);
-                sorted.take(min(a.top_k + 1, L), sub);
-                id = sorted.expert(sub);
-                if (__ballot((sorted.lost || a.top_k == L || !sorted.clear(sub, gap)) && !bad)) {
+                int *const list = (int *)room, taken = min(a.top_k + 1, L);
+                int popped = 0;
+                Sorted::sort(choice, sub, list);
+                bool lost = Sorted::take(choice, popped, 0, taken, sub, list);
+                id = Sorted::expert(list, taken, sub);
+                if (__ballot((lost || a.top_k == L || !Sorted::clear(list, taken, sub, gap)) && !bad)) {
                     if (sigmoid && a.top_k + 4 <= L) {
                         // three candidates more, all in the order of their 64-bit values: whoever is behind
                         // them must lie clearly behind the last choice
                         const int count = a.top_k + 4;
-                        sorted.take(count, sub);
-                        id = sorted.expert(sub);
-                        sure &= !sorted.lost && (!sorted.some(count - 1) ||
-                                                 Sorted::apart(sorted.value(a.top_k - 1), sorted.value(count - 1), gap));
+                        lost |= Sorted::take(choice, popped, taken, count, sub, list);
+                        id = Sorted::expert(list, count, sub);
+                        sure &= !lost && (list[count - 1] <= kNone ||
+                                          Sorted::apart(Sorted::value(list, a.top_k - 1), Sorted::value(list, count - 1), gap));
                         wave_fence();
                         id = order_candidates<LOG>(a, row, sub, count, id, room);
                     } else {
@@ -598,8 +619,10 @@ __global__ __launch_bounds__(kRouteWaves * kWave, R < 16 ? 4 : 3) void route_ker
                 }
                 wave_fence();
             } else {
-#pragma unroll
-                for (int r = 0; r < R; ++r) choice[r] = choice[r] == kNone ? kNone : key_of(l[r]);
+                each<R>([&](auto r) {
+                    const int key = key_of(l[r]), old = choice[r];
+                    choice[r] = old == kNone ? kNone : key;
+                });
                 id = largest_logits<LOG, R>(a, sub, bad, choice, (int *)room);
             }
             if (__ballot(!sure && !bad)) id = choose_wide<LOG, R>(a, sub, top, l, bias, room);
