@@ -538,7 +538,7 @@ def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax", bias
     kind, tokens, experts, stride = _logits(logits, device)
     code = _score(score)
     _buffer(bias, torch.float32, experts, "bias", device, optional=True)
-    shape = (tokens, top_k if top_k > 0 else 0)
+    shape = (tokens, top_k if 0 < top_k <= 64 else 0)  # more are refused below
     ids = _made(ids, torch.int32, shape, tokens * top_k, "ids", logits, device)
     weights = _made(weights, torch.float32, shape, tokens * top_k, "weights", logits, device)
     _check(_lib.loom_route_experts(_ptr(logits), kind, tokens, experts, stride, code, _ptr(bias), groups, top_groups,

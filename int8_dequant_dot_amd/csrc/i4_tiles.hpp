@@ -278,31 +278,48 @@ struct I4TileLoop {
     // Stores the sums r0 .. r0 + N - 1 of each block.  scale_of(r): x_scale of row r of the tile.
     template <int N, typename ScaleOf>
     __device__ __forceinline__ void store(int type, int r0, ScaleOf &&scale_of) {
+        if (type == LOOM_F32) store_as<N>((float *)p.out, r0, scale_of);
+        else if (type == LOOM_F16) store_as<N>((_Float16 *)p.out, r0, scale_of);
+        else store_as<N>((__bf16 *)p.out, r0, scale_of);
+    }
+    template <int N, typename T, typename ScaleOf>
+    __device__ __forceinline__ void store_as(T *out, int r0, ScaleOf &&scale_of) {
+        constexpr int OUT = C::GATED ? 1 : C::WT;  // of a wave's blocks of channels
+        const int64_t n = n0 + (C::GATED ? wm * 32 + m : wm * C::WT * 32 + m);
+        float bias[OUT];
+#pragma unroll
+        for (int w = 0; w < OUT; ++w)
+            bias[w] = !C::GATED && p.bias ? p.bias[(int64_t)expert * p.rows + min(n + w * 32, (int64_t)p.rows - 1)] : 0.0f;
 #pragma unroll
         for (int x = 0; x < C::XT; ++x) {
             const int first = (wn * C::XT + x) * 32;
             if (first >= rows) return;
-            const float xs = scale_of(min(first + m, rows - 1));
+            const float xs = scale_of(min(first + m, rows - 1)) * kI4Unit;
+            T *to = out + (t0 + first + 4 * half) * p.out_stride + n;
+            const int limit = rows - first - 4 * half;
+            float y[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const int r = r0 + e, row = 8 * (r >> 2) + 4 * half + (r & 3);
-                const float scale = __shfl(xs, row);
-                const int64_t out = (t0 + first + row) * p.out_stride;
-                const bool live = first + row < rows;
-                if constexpr (C::GATED) {
-                    const int64_t n = n0 + wm * 32 + m;
-                    const float y = act_value(p.act, acc[x][0][e] * kI4Unit * scale) * (acc[x][1][e] * kI4Unit * scale);
-                    if (live && n < p.rows) store1(p.out, type, out + n, y);
-                } else {
+                const int r = r0 + e;
+                y[e] = __shfl(xs, 8 * (r >> 2) + (r & 3) + 4 * half);
+            }
+            if constexpr (C::GATED) {
+                with_activation(p.act, [&](auto act) {
 #pragma unroll
-                    for (int w = 0; w < C::WT; ++w) {
-                        const int64_t n = n0 + (wm * C::WT + w) * 32 + m;
-                        float y = acc[x][w][e] * kI4Unit * scale;
-                        if (live && n < p.rows) {
-                            if (p.bias) y = y + p.bias[(int64_t)expert * p.rows + n];
-                            store1(p.out, type, out + n, y);
-                        }
-                    }
+                    for (int e = 0; e < N; ++e)
+                        acc[x][0][e] = act_value(decltype(act)::value, acc[x][0][e] * y[e]) * (acc[x][C::WT - 1][e] * y[e]);
+                });
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const int r = r0 + e, row = 8 * (r >> 2) + (r & 3);
+                T *at = to + row * p.out_stride;
+#pragma unroll
+                for (int w = 0; w < OUT; ++w) {
+                    float v = acc[x][w][e];
+                    if constexpr (!C::GATED) v = v * y[e];
+                    if (!C::GATED && p.bias) v = v + bias[w];
+                    if (row < limit && n + w * 32 < p.rows) at[w * 32] = (T)v;
                 }
             }
         }
