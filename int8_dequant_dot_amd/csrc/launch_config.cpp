@@ -215,6 +215,7 @@ int geo_group_routes(const int64_t *w, loom_launch_config *c) {
 template <bool ROUTED, bool GATED>
 int geo_i4(const int64_t *w, loom_launch_config *c) {
     if (w[0] < 0 || w[1] < 0 || w[1] > kI4MaxK || w[2] < 0 || w[3] < 32) return LOOM_ERR_RANGE;
+    if (w[0] > 0x7FFFFFFF || w[2] > 0x7FFFFFFF) return LOOM_ERR_RANGE;
     if (ROUTED && (w[4] < 1 || w[4] > kI4MaxExperts)) return LOOM_ERR_RANGE;
     const int64_t experts = ROUTED ? w[4] : 0;
     int shift = 0;  // log2 of a group's 32-element chunks

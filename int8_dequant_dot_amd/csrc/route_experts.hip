@@ -12,7 +12,7 @@
 // bits.  Weights are f32.
 //
 // The vector unit bounds it: 65536 tokens x 256 experts in f32, the 8 best of 4 of 8
-// groups by sigmoid and bias, take 54 to 60 us, where their 71 MB would take 15; a wave
+// groups by sigmoid and bias, take 51 to 59 us, where their 71 MB would take 15; a wave
 // of four tokens runs 1.4 thousand instructions.  16 lanes hold a token where there are
 // many (fewer cross-lane steps a token), 64 where there are few.  With every choice in 64
 // bits the same took 190 us.
