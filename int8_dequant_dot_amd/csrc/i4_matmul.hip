@@ -142,7 +142,9 @@ __global__ __launch_bounds__(kWave * kI4StreamWaves, 2) void i4_stream_kernel(I4
 #pragma unroll
         for (int i = 0; i < RI; ++i) {
             q.w[i] = there ? wbase[i >= RI / 2][wrow[i] + (uint32_t)(all * 16)] : int4v{};
-            q.scale[i] = sbase[i >= RI / 2][srow[i] + (uint32_t)min((all * 16 + group_at) >> p.chunk_shift, p.groups - 1)];
+            // no group, no scale: a sum of 0 stays 0 whatever the last group's scale is
+            q.scale[i] = (Scale)0.0f;
+            if (all * 16 + group_at < p.chunks) q.scale[i] = sbase[i >= RI / 2][srow[i] + (uint32_t)((all * 16 + group_at) >> p.chunk_shift)];
         }
 #pragma unroll
         for (int v = 0; v < VG; ++v) {

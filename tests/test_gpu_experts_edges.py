@@ -1,0 +1,41 @@
+"""Where the router's f32 choices and the 4-bit products come to their ends: groups whose values nearly tie, biases of the
+lowest value, infinite and vanishing scales, offsets that overlap.  Against 64-bit values, tolerances as in
+test_gpu_experts.py."""
+import pytest
+import torch
+
+from tests.test_gpu_experts import F16, F32, INF, bounded, check, loom, offsets_of, operands, parts, product64  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ scales at the ends of their range
+
+SIZES = [(70, 1056, 32), (70, 544, 32), (70, 1056, 64), (70, 544, 64), (70, 32, 32), (70, 1056, 128), (70, 672, 128),
+         (70, 2080, 256), (40, 4192, 512)]
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 3, 7, 8, 9, 40, 300])
+@pytest.mark.parametrize("rows,k,group", SIZES)
+def test_infinite_scales(loom, device, rows, k, group, tokens):  # noqa: F811
+    """An infinite scale of a row's last group makes its channel infinite, of the sign that the group's sum has; no other
+    channel sees it.  The same at every token count.  (The last groups here are at most 128 long: longer ones are added in
+    parts, which may be infinite in both directions.)"""
+    for scales in (F32, F16):
+        s = operands(2, rows, k, tokens, group, scales, rows + k + tokens)
+        last = slice((k - 1) // group * group, k)
+        s["w"][:, :, last] = s["w"][:, :, last].abs() + 1
+        s["x"][:, last] = s["x"][:, last].clamp(-127, 127).abs() + (s["x"][:, last] == 0)
+        s["w"].clamp_(-8, 7)
+        s["ws"][:, 3, -1], s["ws"][:, 64 if rows > 64 else 33, -1] = INF, -INF
+        want = torch.zeros(rows)
+        want[3], want[64 if rows > 64 else 33] = INF, -INF
+        other = want == 0
+        d = {n: t.to(device) for n, t in s.items()}
+        w, x = loom.pack_int4(d["w"]), loom.pack_int8(d["x"])
+        got = [loom.i4_matmul(w[1], d["ws"][1], x, group=group, dtype=F32).cpu(),
+               loom.i4_expert_matmul(w, d["ws"], x, None, offsets_of([0, tokens]).to(device), group=group, dtype=F32).cpu()]
+        y, size = product64(s["x"], s["w"][1], s["ws"][1].float().clamp(-1, 1), group)
+        for out in got:
+            assert torch.equal(out[:, ~other], want[~other].expand(tokens, -1))
+            check(out[:, other], *(t[:, other] for t in bounded(y, size, parts(k, group), None, None, F32)))
