@@ -514,7 +514,8 @@ int loom_group_routes(const int32_t *ids, int64_t tokens, int64_t routes, int64_
  *     out[t][n] = (sum_g scale[n][g] * f32(acc[t][n][g])) * x_scale[t] + bias[n] *
  * in f32 (the sum over groups in a fixed order), rounded once to the output  *
  * type; a NULL x_scale or bias leaves its operation out.  A group longer than *
- * 128 is the f32 sum of its parts of 128, each of which is exact.           *
+ * 128 is the f32 sum of its parts of 128, each of which is exact.  Sums      *
+ * before x_scale are held 16 times as large: from 2^124 on they overflow.    *
  * Packed 4-bit weights: two's complement, 32 neighbours of k in 16 bytes;    *
  * byte b of them holds element b in its low four bits and element 16 + b in  *
  * its high four.                                                            *

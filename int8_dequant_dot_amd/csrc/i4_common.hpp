@@ -10,8 +10,9 @@ typedef int int16v __attribute__((ext_vector_type(16)));
 
 // 16 bytes of packed weights are 32 neighbours of k: byte b holds element b in
 // its low half and element 16 + b in its high half.  Each half is moved into the
-// high bits of a byte, where it is the int8 16 q: sums carry that factor 16 and
-// are brought back by an exact product with 1/16.
+// high bits of a byte, where it is the int8 16 q: sums carry that factor 16 (so
+// they overflow from 2^124 on) and are brought back by a product with 1/16, exact
+// for all that f32 holds in full.
 constexpr int kI4High = (int)0xF0F0F0F0;
 constexpr float kI4Unit = 0.0625f;
 __device__ __forceinline__ int4v i4_low(int4v w) { return (w << 4) & kI4High; }

@@ -275,7 +275,8 @@ struct I4TileLoop {
         }
     }
 
-    // Stores the sums r0 .. r0 + N - 1 of each block.  scale_of(r): x_scale of row r of the tile.
+    // Stores the sums r0 .. r0 + N - 1 of each block.  scale_of(r): x_scale of row r of the tile, which
+    // may be subnormal: the factor kI4Unit would cost it bits, so the sums take it.
     template <int N, typename ScaleOf>
     __device__ __forceinline__ void store(int type, int r0, ScaleOf &&scale_of) {
         if (type == LOOM_F32) store_as<N>((float *)p.out, r0, scale_of);
@@ -294,7 +295,7 @@ struct I4TileLoop {
         for (int x = 0; x < C::XT; ++x) {
             const int first = (wn * C::XT + x) * 32;
             if (first >= rows) return;
-            const float xs = scale_of(min(first + m, rows - 1)) * kI4Unit;
+            const float xs = scale_of(min(first + m, rows - 1));
             T *to = out + (t0 + first + 4 * half) * p.out_stride + n;
             const int limit = rows - first - 4 * half;
             float y[N];
@@ -307,7 +308,7 @@ struct I4TileLoop {
                 with_activation(p.act, [&](auto act) {
 #pragma unroll
                     for (int e = 0; e < N; ++e)
-                        acc[x][0][e] = act_value(decltype(act)::value, acc[x][0][e] * y[e]) * (acc[x][C::WT - 1][e] * y[e]);
+                        acc[x][0][e] = act_value(decltype(act)::value, acc[x][0][e] * kI4Unit * y[e]) * (acc[x][C::WT - 1][e] * kI4Unit * y[e]);
                 });
             }
 #pragma unroll
@@ -317,7 +318,7 @@ struct I4TileLoop {
 #pragma unroll
                 for (int w = 0; w < OUT; ++w) {
                     float v = acc[x][w][e];
-                    if constexpr (!C::GATED) v = v * y[e];
+                    if constexpr (!C::GATED) v = v * kI4Unit * y[e];
                     if (!C::GATED && p.bias) v = v + bias[w];
                     if (row < limit && n + w * 32 < p.rows) at[w * 32] = (T)v;
                 }

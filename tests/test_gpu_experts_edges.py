@@ -39,3 +39,41 @@ def test_infinite_scales(loom, device, rows, k, group, tokens):  # noqa: F811
         for out in got:
             assert torch.equal(out[:, ~other], want[~other].expand(tokens, -1))
             check(out[:, other], *(t[:, other] for t in bounded(y, size, parts(k, group), None, None, F32)))
+
+
+@pytest.mark.parametrize("tokens", [1, 8, 9, 40, 129, 300, 1000])
+def test_vanishing_activation_scales(loom, device, tokens):  # noqa: F811
+    """Scales of rows that are all but zero lie below the smallest normal f32: they are used as they are.  Sums and results
+    here are whole multiples of powers of two, so they are exact in f32."""
+    rows, k, group = 1100, 320, 128
+    g = torch.Generator().manual_seed(tokens)
+    wq = torch.randint(-8, 8, (2, rows, k), generator=g, dtype=torch.int8)
+    xq = torch.randint(-20, 21, (tokens, k), generator=g, dtype=torch.int8)
+    ws = torch.full((2, rows, 3), 2.0 ** 100)
+    step = 2.0 ** -149
+    xs = (torch.randint(1, 8, (tokens,), generator=g).double() * step).float()
+    w, x = loom.pack_int4(wq.to(device)), loom.pack_int8(xq.to(device))
+    offsets = offsets_of([0, tokens]).to(device)
+    want = (xq.double() @ wq[1].double().t()) * 2.0 ** 100 * xs.double()[:, None]
+    got = [loom.i4_matmul(w[1], ws[1].to(device), x, xs.to(device), group=group, dtype=F32),
+           loom.i4_expert_matmul(w, ws.to(device), x, xs.to(device), offsets, group=group, dtype=F32),
+           loom.i4_expert_gated_projection(w, ws.to(device), w, ws.to(device), x, xs.to(device), offsets, act="relu", group=group,
+                                           dtype=F32)]
+    assert bool((xs > 0).all()) and torch.equal(got[0].cpu().double(), want) and torch.equal(got[1].cpu().double(), want)
+    both = want.clamp(min=0) * want  # about 2^-60: one rounding
+    assert bool(((got[2].cpu().double() - both).abs() <= 2.0 ** -24 * both.abs()).all())
+
+
+@pytest.mark.parametrize("tokens", [1, 8, 9, 40, 129, 300, 1000])
+def test_large_sums(loom, device, tokens):  # noqa: F811
+    """Sums of just less than 2^124, before an activation's scale brings them back, are exact too."""
+    rows, k, group = 1100, 320, 128
+    g = torch.Generator().manual_seed(tokens)
+    wq = torch.randint(-8, 8, (rows, k), generator=g, dtype=torch.int8)
+    xq = torch.randint(-20, 21, (tokens, k), generator=g, dtype=torch.int8)
+    ws, xs = torch.full((rows, 3), 2.0 ** 108), torch.full((tokens,), 2.0 ** -90)
+    assert 8 * 20 * k < 2 ** 16
+    want = (xq.double() @ wq.double().t()) * 2.0 ** 18
+    got = loom.i4_matmul(loom.pack_int4(wq.to(device)), ws.to(device), loom.pack_int8(xq.to(device)), xs.to(device), group=group,
+                         dtype=F32)
+    assert torch.equal(got.cpu().double(), want)
