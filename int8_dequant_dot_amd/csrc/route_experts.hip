@@ -177,23 +177,32 @@ __device__ __forceinline__ void merge_two(int &first, int &second) {
 
 // Takes the choices of all but the best groups away: a group's value is its largest
 // choice, or the sum of its two largest, and a group stays while fewer than top_groups
-// are better.  margin: how far the worst of those that stay lies above the best of
-// the others (groups without a choice apart: it does not matter whether they stay).
-// room: LDS of this token, experts + 2 groups values.
-template <int LOG, int R>
-__device__ __forceinline__ void best_groups(const RouteArgs &a, int sub, float *room, int (&c)[R], float &margin) {
+// are better.  Returns whether the order of 64-bit values keeps the same ones (true where
+// COMPUTED is false: logits are what they are): whether the least that one that stays can be
+// lies above the most that another can be (groups without a choice apart: it does not matter
+// whether they stay).  A group's value is off by its scores' errors, `gap` at most, by the
+// choices' roundings, 2^-24 of each, and the sum's, 2^-24 of it: by less than 2^-23 of the
+// choices' magnitudes, and twice that leaves room for the bounds' own roundings.
+// room: LDS of this token, experts + 3 groups values.
+template <bool COMPUTED, int LOG, int R>
+__device__ __forceinline__ bool best_groups(const RouteArgs &a, int sub, float *room, int (&c)[R], float gap) {
     typedef Held<LOG, R> H;
     constexpr int L = H::L, B = (R + 3) / 4;
     const int size = a.experts / a.groups;
     int *const ranks = (int *)room + a.experts;
-    auto value = [&](int first, int second) {
-        return a.group_top > 1 && second > kNone ? key_of(of_key(first) + of_key(second)) : first;
+    float *const sizes = room + a.experts + 2 * a.groups;
+    auto rank = [&](int g, int first, int second) {
+        const bool both = a.group_top > 1 && second > kNone;
+        ranks[g] = both ? key_of(of_key(first) + of_key(second)) : first;
+        if (COMPUTED) sizes[g] = fabsf(of_key(first)) + (both ? fabsf(of_key(second)) : 0.0f);
     };
-    int worst = 0x7FFFFFFF, best = kNone;
-    auto weigh = [&](bool stays, int mine) {
-        if (mine > kNone) {
-            worst = stays ? min(worst, mine) : worst;
-            best = stays ? best : max(best, mine);
+    float worst = kInf, best = -kInf;
+    auto weigh = [&](bool stays, int g) {
+        const int mine = ranks[g];
+        if (COMPUTED && mine > kNone) {
+            const float value = of_key(mine), off = sizes[g] * 0x1p-22f + gap;
+            worst = stays ? fminf(worst, value - off) : worst;
+            best = stays ? best : fmaxf(best, value + off);
         }
     };
     if (H::V == 4 && size >= 4 && size <= 4 * L && (size & (size - 1)) == 0) {
@@ -216,7 +225,7 @@ __device__ __forceinline__ void best_groups(const RouteArgs &a, int sub, float *
             }
             const int e = H::expert_at(4 * b, sub);
             group[b] = e >> shift;
-            if (e < a.experts && (e & (size - 1)) == 0) ranks[group[b]] = value(first, second);
+            if (e < a.experts && (e & (size - 1)) == 0) rank(group[b], first, second);
         }
         wave_fence();
         // a lane a group: how many are better (equal and before it, or greater)
@@ -224,7 +233,7 @@ __device__ __forceinline__ void best_groups(const RouteArgs &a, int sub, float *
             const int that = ranks[g];
             int better = 0;
             for (int o = 0; o < a.groups; ++o) better += ranks[o] - (o >= g) >= that;
-            weigh(better < a.top_groups, that);
+            weigh(better < a.top_groups, g);
             ranks[a.groups + g] = better;
         }
         wave_fence();
@@ -247,7 +256,7 @@ __device__ __forceinline__ void best_groups(const RouteArgs &a, int sub, float *
         for (int g = sub; g < a.groups; g += L) {
             int first = kNone, second = kNone;
             for (int i = 0; i < size; ++i) keep_two(values[g * size + i], first, second);
-            ranks[g] = value(first, second);
+            rank(g, first, second);
         }
         wave_fence();
         // each group's verdict, then each expert's
@@ -257,7 +266,7 @@ __device__ __forceinline__ void best_groups(const RouteArgs &a, int sub, float *
                 const int mine = ranks[g];
                 int better = 0;
                 for (int o = 0; o < a.groups; ++o) better += ranks[o] - (o >= g) >= mine;
-                weigh(better < a.top_groups, mine);
+                weigh(better < a.top_groups, g);
                 if (better >= a.top_groups)
                     for (int i = 0; i < size; ++i) values[g * size + i] = kNone;
             }
@@ -267,8 +276,10 @@ __device__ __forceinline__ void best_groups(const RouteArgs &a, int sub, float *
         for (int r = 0; r < R; ++r)
             if (H::expert_at(r, sub) < a.experts) c[r] = values[H::expert_at(r, sub)];
     }
-    margin = of_key(fold_min<LOG>(worst)) - of_key(fold_max<LOG>(best));
     wave_fence();  // the room may be written again
+    if (!COMPUTED) return true;
+    best = fold_max<LOG>(best);
+    return best == -kInf || -fold_max<LOG>(-worst) > best;
 }
 
 // The top_k largest choices, lane i keeping the i-th's expert, -1 where there is none.
@@ -574,13 +585,11 @@ __global__ __launch_bounds__(kRouteWaves * kWave, R == 16 ? (LOG == 4 ? 3 : 2) :
             total = fold_sum<LOG>(sum);
         }
         int id;
-        float margin;
         if (computed) {
             // In f32 first.  A sigmoid's error is below 2^-22 (the exponential's relative error, (1.3 |l| + 2)
             // 2^-24, counts s (1 - s) times, and |l| s (1 - s) < 0.23; the reciprocal's is 2^-23), a softmax's below
             // 2^-18 of it (31 additions, the terms' 2^-22 and a mean distance of at most 7 from the largest), and
-            // the bias rounds to 2^-24 of |c|: where choices or groups lie `gap` apart their order is that of the
-            // 64-bit values.
+            // the bias rounds to 2^-24 of |c|: where choices lie `gap` apart their order is that of the 64-bit values.
             const float unit = 1.0f / total;  // a softmax's largest score
             const float gap = (sigmoid ? 0x1p-21f : unit * 0x1p-17f) + largest_bias * 0x1p-23f;
             int choice[R];
@@ -591,10 +600,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave, R == 16 ? (LOG == 4 ? 3 : 2) :
                 choice[r] = l[r] == -kInf ? kNone : key;
             });
             bool sure = true;
-            if (a.groups > 1) {
-                best_groups<LOG, R>(a, sub, (float *)room, choice, margin);
-                sure = margin > 2 * gap;
-            }
+            if (a.groups > 1) sure = best_groups<true, LOG, R>(a, sub, (float *)room, choice, gap);
             if (a.bias) {
                 typedef SortedChoice<false, LOG, R> Sorted;
                 int *const list = (int *)room, taken = min(a.top_k + 1, L);
@@ -630,7 +636,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave, R == 16 ? (LOG == 4 ? 3 : 2) :
             int c[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) c[r] = key_of(l[r]);
-            if (a.groups > 1) best_groups<LOG, R>(a, sub, (float *)room, c, margin);
+            if (a.groups > 1) best_groups<false, LOG, R>(a, sub, (float *)room, c, 0.0f);
             id = largest_logits<LOG, R>(a, sub, bad, c, (int *)room);
         }
         const bool live = id >= 0 && sub < a.top_k;

@@ -9,6 +9,72 @@ from tests.test_gpu_experts import F16, F32, INF, bounded, check, loom, offsets_
 pytestmark = pytest.mark.gpu
 
 
+# ------------------------------------------------------------------ groups that nearly tie
+
+def best_of_two_groups(logits, bias):
+    """The two experts of the better of two groups of two, falling, from 64-bit choices (sigmoid and bias)."""
+    c = torch.sigmoid(logits.double()) + bias.double()
+    first = (c[:, 2] + c[:, 3]) > (c[:, 0] + c[:, 1])
+    ids = torch.empty(len(logits), 2, dtype=torch.int32)
+    for g in (0, 1):
+        pair = torch.where((c[:, 2 * g + 1] > c[:, 2 * g])[:, None], torch.tensor([2 * g + 1, 2 * g]), torch.tensor([2 * g, 2 * g + 1]))
+        ids[first == bool(g)] = pair.to(torch.int32)[first == bool(g)]
+    return ids
+
+
+def check_groups(loom, device, logits, bias):  # noqa: F811
+    """As groups of two, and as groups of eight whose other experts are masked; as a batch, and a few tokens at a time."""
+    want = best_of_two_groups(logits, bias)
+    wide, wide_bias = torch.full((len(logits), 16), -INF), torch.zeros(16)
+    at = torch.tensor([1, 6, 10, 13])
+    wide[:, at], wide_bias[at] = logits, bias
+    for few in (False, True):
+        def ids(l, b):
+            l, b = l.to(device), b.to(device)
+            runs = l.split(600) if few else [l]
+            return torch.cat([loom.route_experts(r, 2, "sigmoid", b, 2, 1, 2)[0] for r in runs]).cpu()
+        assert torch.equal(ids(logits, bias), want)
+        assert torch.equal(ids(wide, wide_bias), at.to(torch.int32)[want.long()])
+
+
+@pytest.mark.parametrize("step", [2.0 ** -21, 2.0 ** -20, 2.0 ** -19])
+def test_groups_near_half_steps(loom, device, step):  # noqa: F811
+    """Choices next to half steps of f32, in sums that round in opposite directions: the worst of f32 for two groups."""
+    c = step * 2.0 ** 23 + (torch.tensor([1001, 2000, 1600, 1401], dtype=torch.float64) + 0.5) * step
+    near = c - 0.8 + 0.005 * torch.arange(4)
+    bias = (near / (step / 2)).round() * (step / 2)  # held exactly
+    l = torch.logit(c - bias).float()
+    j = torch.arange(-6, 7)
+    grid = torch.cartesian_prod(j, j, j, j)
+    logits = (l.view(torch.int32)[None] + grid.to(torch.int32)).view(F32).contiguous()
+    check_groups(loom, device, logits, bias.float())
+    swap = torch.tensor([2, 3, 0, 1])
+    check_groups(loom, device, logits[:, swap].contiguous(), bias.float()[swap])
+
+
+@pytest.mark.parametrize("size", [0.25, 7.0, 100.0, 1000.0, 30000.0])
+def test_groups_near_ties(loom, device, size):  # noqa: F811
+    """Random tokens whose second group is moved to within a few steps of the first."""
+    g = torch.Generator().manual_seed(int(size))
+    bias = size * (1 + 1e-4 * torch.rand(4, generator=g))
+    bias[3] = (bias[0].double() + bias[1].double() - bias[2].double()).float()
+    s = 0.3 + 0.4 * torch.rand(20000, 4, generator=g, dtype=torch.float64)
+    b = bias.double()
+    s[:, 3] = s[:, 0] + s[:, 1] - s[:, 2] + (b[0] + b[1] - b[2] - b[3])
+    s = s[(s[:, 3] > 0.05) & (s[:, 3] < 0.95)]
+    logits = torch.logit(s).float()
+    logits[:, 3] = (logits[:, 3].view(torch.int32) + torch.randint(-8, 9, (len(s),), generator=g, dtype=torch.int32)).view(F32)
+    assert len(s) > 5000
+    check_groups(loom, device, logits, bias)
+
+
+def test_groups_one_token(loom, device):  # noqa: F811
+    """Second group ahead by 2.2e-7, the first by 3.8e-6 if every step is rounded to f32."""
+    logits = torch.tensor([[float.fromhex(v) for v in ("0x1.731936p0", "0x1.697162p0", "0x1.6cb4c4p0", "0x1.700cf4p0")]])
+    bias = torch.tensor([7.19006395, 7.19593716, 7.19393682, 7.19190359])
+    check_groups(loom, device, logits, bias)
+
+
 # ------------------------------------------------------------------ scales at the ends of their range
 
 SIZES = [(70, 1056, 32), (70, 544, 32), (70, 1056, 64), (70, 544, 64), (70, 32, 32), (70, 1056, 128), (70, 672, 128),
