@@ -159,6 +159,8 @@ __device__ __forceinline__ int key_of(float v) {
 }
 __device__ __forceinline__ float of_key(int k) { return __builtin_bit_cast(float, k ^ (int)((uint32_t)(k >> 31) >> 1)); }
 constexpr int kNone = (int)0x807FFFFF;  // key_of(-infinity)
+constexpr int kPast = 0x7FFFFFFF;       // past key_of(infinity)
+constexpr float kMost = 0x1.fffffep127f;  // the largest finite value
 
 // The two largest of a lane's and of 2^STEPS lanes' values.
 __device__ __forceinline__ void keep_two(int v, int &first, int &second) {
@@ -193,16 +195,19 @@ __device__ __forceinline__ bool best_groups(const RouteArgs &a, int sub, float *
     float *const sizes = room + a.experts + 2 * a.groups;
     auto rank = [&](int g, int first, int second) {
         const bool both = a.group_top > 1 && second > kNone;
-        ranks[g] = both ? key_of(of_key(first) + of_key(second)) : first;
+        // a sum below the lowest f32 value is not that of a group without choices
+        ranks[g] = both ? max(key_of(of_key(first) + of_key(second)), kNone + 1) : first;
         if (COMPUTED) sizes[g] = fabsf(of_key(first)) + (both ? fabsf(of_key(second)) : 0.0f);
     };
-    float worst = kInf, best = -kInf;
+    int worst = kPast, best = kNone;
     auto weigh = [&](bool stays, int g) {
         const int mine = ranks[g];
         if (COMPUTED && mine > kNone) {
-            const float value = of_key(mine), off = sizes[g] * 0x1p-22f + gap;
-            worst = stays ? fminf(worst, value - off) : worst;
-            best = stays ? best : fmaxf(best, value + off);
+            // sums beyond the largest f32 value may be anything beyond it
+            const float value = of_key(mine), off = fminf(sizes[g], kMost) * 0x1p-22f + gap;
+            const float least = value > -kMost ? fminf(value, kMost) - off : -kInf;
+            worst = stays ? min(worst, key_of(least)) : worst;
+            best = stays ? best : max(best, key_of(value + off));
         }
     };
     if (H::V == 4 && size >= 4 && size <= 4 * L && (size & (size - 1)) == 0) {
@@ -279,7 +284,7 @@ __device__ __forceinline__ bool best_groups(const RouteArgs &a, int sub, float *
     wave_fence();  // the room may be written again
     if (!COMPUTED) return true;
     best = fold_max<LOG>(best);
-    return best == -kInf || -fold_max<LOG>(-worst) > best;
+    return best == kNone || fold_min<LOG>(worst) > best;
 }
 
 // The top_k largest choices, lane i keeping the i-th's expert, -1 where there is none.

@@ -4,9 +4,11 @@ test_gpu_experts.py."""
 import pytest
 import torch
 
-from tests.test_gpu_experts import F16, F32, INF, bounded, check, loom, offsets_of, operands, parts, product64  # noqa: F401
+from tests.test_gpu_experts import (F16, F32, INF, bounded, check, check_route, loom, offsets_of, operands,  # noqa: F401
+                                       parts, product64)
 
 pytestmark = pytest.mark.gpu
+LOWEST = torch.finfo(F32).min
 
 
 # ------------------------------------------------------------------ groups that nearly tie
@@ -73,6 +75,31 @@ def test_groups_one_token(loom, device):  # noqa: F811
     logits = torch.tensor([[float.fromhex(v) for v in ("0x1.731936p0", "0x1.697162p0", "0x1.6cb4c4p0", "0x1.700cf4p0")]])
     bias = torch.tensor([7.19006395, 7.19593716, 7.19393682, 7.19190359])
     check_groups(loom, device, logits, bias)
+
+
+# ------------------------------------------------------------------ biases of the lowest value
+
+@pytest.mark.parametrize("tokens", [9, 1100])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_of_lowest_biases(loom, device, score, tokens):  # noqa: F811
+    """Groups whose two best choices add up to less than the lowest f32 value are groups all the same: better than those
+    whose experts are all masked, in the order of their 64-bit sums."""
+    for size, kept in ((2, 3), (8, 3), (8, 5)):
+        experts = 6 * size
+        g = torch.Generator().manual_seed(size)
+        logits = torch.randn(tokens, experts, generator=g)
+        logits[:, :size] = -INF                        # group 0: nothing
+        bias = torch.zeros(experts)
+        bias[size:2 * size] = LOWEST                   # 1: the lowest value throughout
+        bias[2 * size:3 * size] = -2.5e38              # 2: lower sum than 3
+        bias[3 * size:4 * size] = -2.0e38
+        bias[4 * size:5 * size] = LOWEST               # 4: one expert is not
+        bias[4 * size] = 0.5
+        bias[5 * size] = LOWEST                        # 5: one expert is
+        check_route(loom, device, logits.to(device), 3, score, bias, 6, kept, 2)
+        check_route(loom, device, logits.to(device), 2 * size, score, bias, 6, kept, 2, False)
+        check_route(loom, device, logits.to(device), min(3, size), score, -bias, 6, 1, 2)  # and sums beyond the largest
+        check_route(loom, device, logits.to(device), 3, score, -bias, 6, kept, 2)
 
 
 # ------------------------------------------------------------------ scales at the ends of their range
