@@ -393,7 +393,10 @@ struct SortedChoice {
         return lost || (D < R && popped >= D);  // this lane's list is used up, its keys may not be
     }
     static __device__ __forceinline__ float value(const int *room, int i) { return of_key(room[i] & ~LOW); }
+    // Whether choices with these keys lie apart.  The low bits that hold R numbers are up to (R - 1) 2^-23
+    // of the choice, its own rounding 2^-24 of it: with 16, 15.5 of the 16 2^-23 here.
     static __device__ __forceinline__ bool apart(float high, float low, float gap) {
+        static_assert(EXACT || R <= 16, "the bits that keys lose");
         return high - low > gap + 0x1p-19f * (fabsf(high) + fabsf(low));
     }
     // Whether the choice after lane sub's lies apart from it, or there is none.
@@ -547,18 +550,14 @@ __global__ __launch_bounds__(kRouteWaves * kWave, R == 16 ? (LOG == 4 ? 3 : 2) :
     const bool sigmoid = a.score == LOOM_SIGMOID;
     // choices, or groups' values, that are computed; else logits, which need no rounding
     const bool computed = a.bias || (a.groups > 1 && a.group_top > 1);
-    float bias[R], largest_bias = 0.0f;
+    float bias[R];
     bool odd = false;
 #pragma unroll
     for (int r = 0; r < R; ++r) bias[r] = 0.0f;
     if (a.bias) {
         load_row<LOG, R>(a.bias, a.experts, sub, 0.0f, bias);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if (fabsf(bias[r]) < kInf) largest_bias = fmaxf(largest_bias, fabsf(bias[r]));
-            odd |= bias[r] != bias[r];
-        }
-        largest_bias = fold<LOG>(largest_bias, [](float x, float y) { return fmaxf(x, y); });
+        for (int r = 0; r < R; ++r) odd |= bias[r] != bias[r];
     }
     const bool any_odd = __ballot(odd);
     for (int64_t base = (int64_t)blockIdx.x * PER; base < a.tokens; base += (int64_t)gridDim.x * PER) {
@@ -593,10 +592,10 @@ __global__ __launch_bounds__(kRouteWaves * kWave, R == 16 ? (LOG == 4 ? 3 : 2) :
         if (computed) {
             // In f32 first.  A sigmoid's error is below 2^-22 (the exponential's relative error, (1.3 |l| + 2)
             // 2^-24, counts s (1 - s) times, and |l| s (1 - s) < 0.23; the reciprocal's is 2^-23), a softmax's below
-            // 2^-18 of it (31 additions, the terms' 2^-22 and a mean distance of at most 7 from the largest), and
-            // the bias rounds to 2^-24 of |c|: where choices lie `gap` apart their order is that of the 64-bit values.
+            // 2^-18 of it (31 additions, the terms' 2^-22 and a mean distance of at most 7 from the largest): two of
+            // them differ by `gap`.  The sum with the bias rounds to 2^-24 of the choice, which comparisons count.
             const float unit = 1.0f / total;  // a softmax's largest score
-            const float gap = (sigmoid ? 0x1p-21f : unit * 0x1p-17f) + largest_bias * 0x1p-23f;
+            const float gap = sigmoid ? 0x1p-21f : unit * 0x1p-17f;
             int choice[R];
             if (sigmoid) each<R>([&](auto r) { s[r] = loom::sigmoid(l[r]); });
             else each<R>([&](auto r) { s[r] = s[r] * unit; });

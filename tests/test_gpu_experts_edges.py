@@ -102,6 +102,26 @@ def test_groups_of_lowest_biases(loom, device, score, tokens):  # noqa: F811
         check_route(loom, device, logits.to(device), 3, score, -bias, 6, kept, 2)
 
 
+@pytest.mark.parametrize("tokens", [9, 1100])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_lowest_biases_beside_small_ones(loom, device, score, tokens):  # noqa: F811
+    """A few experts shut by the lowest value, the others ordered by ordinary biases, with near ties among them; large
+    biases apart from small ones; tokens without any expert between the others."""
+    experts = 64
+    g = torch.Generator().manual_seed(21)
+    logits = (1 + torch.randint(0, 40, (tokens, experts), generator=g) * 2.0 ** -23).float()
+    logits[::3] = torch.randn(len(logits[::3]), experts, generator=g)
+    logits[4::7] = -INF
+    bias = 0.1 * torch.randn(experts, generator=g)
+    bias[8:16] = bias[:8]
+    bias[[0, 17, 40]] = LOWEST
+    bias[[1, 41]] = -1e9
+    bias[2] = 1e4
+    for groups, kept, top_group in ((1, 1, 1), (8, 3, 1), (8, 3, 2), (32, 9, 2)):
+        check_route(loom, device, logits.to(device), 8, score, bias, groups, kept, top_group)
+        check_route(loom, device, logits.to(device), 8, score, bias, groups, kept, top_group, False)
+
+
 # ------------------------------------------------------------------ scales at the ends of their range
 
 SIZES = [(70, 1056, 32), (70, 544, 32), (70, 1056, 64), (70, 544, 64), (70, 32, 32), (70, 1056, 128), (70, 672, 128),
