@@ -616,8 +616,9 @@ constexpr int64_t gated_backward_workspace_bytes(int64_t rows, int64_t k, int64_
 // The router and its gradient.  A token is held by 2^route_log_lanes lanes.
 constexpr int64_t kRouteMaxExperts = 1024, kRouteMaxTopK = 64, kRouteMaxGroups = 64;
 constexpr int kRouteWaves = 4;
-// 64-bit values of LDS a token: its choices and groups' values, or a candidate a lane.
-constexpr int64_t route_room(int64_t experts, int64_t groups) { return experts + groups > 64 ? experts + groups : 64; }
+// 64-bit values of LDS a token: its choices and groups' values, or a candidate a lane, or the
+// largest choice of 65 and its lane.
+constexpr int64_t route_room(int64_t experts, int64_t groups) { return experts + groups > 65 ? experts + groups : 65; }
 constexpr int route_log_lanes(int64_t tokens, int64_t experts, int64_t top_k) {
     return experts <= 256 && top_k <= 16 && tokens >= 1024 ? 4 : 6;
 }

@@ -352,11 +352,12 @@ __device__ __forceinline__ void sort_heads(int (&k)[R]) {
 // EXACT: keys of 16-bit logits, whose low bits hold the expert, so that they are all
 // different and in the order wanted.  Otherwise the low bits hold which of the lane's
 // it was, and choices that are not `gap` and the bits so lost apart may be in either order.
-// lost: a choice may be missing.  room: LDS of this token, 2 L words.
+// lost: a choice may be missing.  room: LDS of this token, 2 L + 2 words: up to L + 1 choices, so that
+// one behind the last is known where a token's lanes are all taken, and their lanes.
 template <bool EXACT, int LOG, int R>
 struct SortedChoice {
     typedef Held<LOG, R> H;
-    static constexpr int D = R < 8 ? R : 8, LOW = EXACT ? H::L * R - 1 : R - 1;
+    static constexpr int D = R < 8 ? R : 8, LOW = EXACT ? H::L * R - 1 : R - 1, kLanes = H::L + 1;
 
     // Turns keys into this lane's list.
     static __device__ __forceinline__ void sort(int (&h)[R], int sub, int *room) {
@@ -364,10 +365,10 @@ struct SortedChoice {
             h[r] = (h[r] & ~LOW) | (LOW - (EXACT ? H::expert_at(r, sub) : (int)r));
         });
         sort_heads(h);
-        room[sub] = kNone;
+        room[sub] = room[H::L] = kNone;
         wave_fence();
     }
-    // Writes down the choices from..count - 1, count at most L; popped: how many were this lane's.
+    // Writes down the choices from..count - 1, count at most L + 1; popped: how many were this lane's.
     static __device__ __forceinline__ bool take(int (&h)[R], int &popped, int from, int count, int sub, int *room) {
         bool lost = false;
         for (int taken = from; taken < count; ++taken) {
@@ -375,7 +376,7 @@ struct SortedChoice {
             const bool some = best > kNone, hit = some && h[0] == best;
             if (hit) {
                 room[taken] = best;
-                if (!EXACT) room[H::L + taken] = sub;
+                if (!EXACT) room[kLanes + taken] = sub;
             }
             if (!EXACT) {
                 const uint64_t hits = __builtin_amdgcn_ballot_w64(hit), lanes = __builtin_amdgcn_ballot_w64(some);
@@ -406,7 +407,7 @@ struct SortedChoice {
     // Lane sub's choice, -1 where there is none.
     static __device__ __forceinline__ int expert(const int *room, int taken, int sub) {
         const int best = room[sub], low = LOW - (best & LOW);
-        return sub < taken && best > kNone ? (EXACT ? low : H::expert_at(low, room[H::L + sub])) : -1;
+        return sub < taken && best > kNone ? (EXACT ? low : H::expert_at(low, room[kLanes + sub])) : -1;
     }
 };
 
@@ -513,8 +514,7 @@ __device__ __forceinline__ int choose_wide(const RouteArgs &a, int sub, float to
     return id;
 }
 
-// The top_k largest of the logits whose keys these are.  (A top_k of all lanes leaves no
-// room for the choice behind the last.)
+// The top_k largest of the logits whose keys these are.
 template <int LOG, int R>
 __device__ __forceinline__ int largest_logits(const RouteArgs &a, int sub, int bad, int (&c)[R], int *room) {
     int id, h[R], popped = 0;
@@ -522,11 +522,11 @@ __device__ __forceinline__ int largest_logits(const RouteArgs &a, int sub, int b
     each<R>([&](auto r) { h[r] = c[r]; });
     if (a.type == LOOM_F32) {
         typedef SortedChoice<false, LOG, R> Sorted;
-        const int taken = min(a.top_k + 1, 1 << LOG);
+        const int taken = a.top_k + 1;
         Sorted::sort(h, sub, room);
         const bool lost = Sorted::take(h, popped, 0, taken, sub, room);
         id = Sorted::expert(room, taken, sub);
-        sure = !lost && a.top_k < 1 << LOG && Sorted::clear(room, taken, sub, 0.0f);
+        sure = !lost && Sorted::clear(room, taken, sub, 0.0f);
     } else {
         typedef SortedChoice<true, LOG, R> Sorted;
         Sorted::sort(h, sub, room);
@@ -607,12 +607,12 @@ __global__ __launch_bounds__(kRouteWaves * kWave, R == 16 ? (LOG == 4 ? 3 : 2) :
             if (a.groups > 1) sure = best_groups<true, LOG, R>(a, sub, (float *)room, choice, gap);
             if (a.bias) {
                 typedef SortedChoice<false, LOG, R> Sorted;
-                int *const list = (int *)room, taken = min(a.top_k + 1, L);
+                int *const list = (int *)room, taken = a.top_k + 1;
                 int popped = 0;
                 Sorted::sort(choice, sub, list);
                 bool lost = Sorted::take(choice, popped, 0, taken, sub, list);
                 id = Sorted::expert(list, taken, sub);
-                if (__ballot((lost || a.top_k == L || !Sorted::clear(list, taken, sub, gap)) && !bad)) {
+                if (__ballot((lost || !Sorted::clear(list, taken, sub, gap)) && !bad)) {
                     if (sigmoid && a.top_k + 4 <= L) {
                         // three candidates more, all in the order of their 64-bit values: whoever is behind
                         // them must lie clearly behind the last choice

@@ -4,8 +4,8 @@ test_gpu_experts.py."""
 import pytest
 import torch
 
-from tests.test_gpu_experts import (F16, F32, INF, bounded, check, check_route, loom, offsets_of, operands,  # noqa: F401
-                                       parts, product64)
+from tests.test_gpu_experts import (BF16, F16, F32, INF, bounded, check, check_route, loom, offsets_of,  # noqa: F401
+                                       operands, parts, product64)
 
 pytestmark = pytest.mark.gpu
 LOWEST = torch.finfo(F32).min
@@ -120,6 +120,41 @@ def test_lowest_biases_beside_small_ones(loom, device, score, tokens):  # noqa: 
     for groups, kept, top_group in ((1, 1, 1), (8, 3, 1), (8, 3, 2), (32, 9, 2)):
         check_route(loom, device, logits.to(device), 8, score, bias, groups, kept, top_group)
         check_route(loom, device, logits.to(device), 8, score, bias, groups, kept, top_group, False)
+
+
+# ------------------------------------------------------------------ many choices
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("top_k", [11, 12, 13, 14, 15, 16, 17])
+def test_many_choices(loom, device, top_k, score):  # noqa: F811
+    """Batches in which a token's lanes are nearly all taken by its choices, ties and near ties among them."""
+    g = torch.Generator().manual_seed(top_k)
+    logits = torch.randn(1030, 48, generator=g)
+    logits[::5] = (1 + torch.randint(0, 3, (len(logits[::5]), 48), generator=g) * 2.0 ** -23).float()
+    bias = torch.zeros(48)
+    bias[::3] = 2.0 ** -26
+    for groups, kept in ((1, 1), (4, 2)):
+        for dtype in (F32, BF16, F16):
+            check_route(loom, device, logits.to(dtype).to(device), top_k, score, bias, groups, kept)
+            check_route(loom, device, logits.to(dtype).to(device), top_k, score, None, groups, kept, 1, False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("tokens,experts,top_k", [(130, 64, 64), (130, 65, 64), (130, 63, 63), (130, 200, 63), (130, 200, 64),
+                                                  (40, 1000, 64), (1030, 16, 16), (1030, 17, 16), (1030, 250, 16)])
+def test_every_lane_a_choice(loom, device, tokens, experts, top_k, score):  # noqa: F811
+    """As many choices as a token has lanes: one more is looked at, where there is one, and rows with fewer experts end
+    before it."""
+    g = torch.Generator().manual_seed(experts)
+    logits = torch.randn(tokens, experts, generator=g)
+    logits[1::4] = (1 + torch.randint(0, 3, (len(logits[1::4]), experts), generator=g) * 2.0 ** -23).float()
+    logits[2::9, top_k - 1:] = -INF
+    logits[3::9, 5:] = -INF
+    logits[4::9] = -INF
+    bias = 0.1 * torch.randn(experts, generator=g)
+    for dtype in (F32, BF16):
+        check_route(loom, device, logits.to(dtype).to(device), top_k, score, bias)
+        check_route(loom, device, logits.to(dtype).to(device), top_k, score, None, renormalize=False)
 
 
 # ------------------------------------------------------------------ scales at the ends of their range
