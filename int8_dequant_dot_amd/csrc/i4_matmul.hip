@@ -267,11 +267,14 @@ hipError_t run(const loom_launch_config &cfg, const I4Product &p, int type, hipS
     const dim3 grid(cfg.workgroups[0]), block(cfg.workgroup_size[0]);
     const int64_t experts = ROUTED ? p.experts : 0;
     const int subs = i4_subs(p.chunk_shift), slots = i4_stream_slots(p.tokens, experts, subs);
-    if (slots == 4) hipLaunchKernelGGL((i4_stream_kernel<ROUTED, GATED, ST, 1>), grid, block, 0, stream, p, type);
-    else if (slots == 8) hipLaunchKernelGGL((i4_stream_kernel<ROUTED, GATED, ST, 2>), grid, block, 0, stream, p, type);
-    else
+    if (slots == 4) {
+        hipLaunchKernelGGL((i4_stream_kernel<ROUTED, GATED, ST, 1>), grid, block, 0, stream, p, type);
+    } else if (slots == 8) {  // dense only
+        if constexpr (!ROUTED) hipLaunchKernelGGL((i4_stream_kernel<false, false, ST, 2>), grid, block, 0, stream, p, type);
+    } else {
         launch_tile<ROUTED, GATED, ST>(i4_tile_choice(p.rows, 32 * (int64_t)p.chunks, p.tokens, experts, GATED, subs), subs, grid,
                                        block, p, type, stream);
+    }
     return hipGetLastError();
 }
 
