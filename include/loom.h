@@ -548,8 +548,9 @@ int loom_i4_matmul(const int32_t *w, const void *w_scale, int scale_type, int64_
  *     out[p][n] = loom_i4_matmul's for w[e], w_scale[e], bias[e], x[index[p]] *
  * Rows of out that belong to no expert are left as they were.  offsets may   *
  * name any rows: only those within [0, pairs) count, and an expert whose     *
- * offsets fall has none; rows that several experts claim have no defined     *
- * value.  A row whose index is outside [0, x_rows) becomes NaN.              *
+ * offsets fall has none.  Where ranges of experts overlap, no row of any     *
+ * expert has a defined value, and each may be left as it was.  A row whose   *
+ * index is outside [0, x_rows) becomes NaN.                                 *
  *   w          : int32[experts][rows][k/8], w_scale : scale_type[experts]    *
  *                [rows][ceil(k / group)], bias : f32[experts][rows] or NULL   *
  *   x          : int32[x_rows][k/4], x_scale : f32[x_rows] or NULL           *

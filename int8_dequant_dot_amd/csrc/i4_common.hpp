@@ -38,7 +38,8 @@ __device__ __forceinline__ int wave_scan(int v) {
 // Tile `index` of the routes grouped by expert, in tiles of up to `size` rows of
 // one expert: which expert, its first row and how many.  Every lane takes part
 // and returns the same; false past the last tile.  offsets that are out of order
-// or out of range make an expert's rows fewer, never others.
+// or out of range make an expert's rows fewer, never others; where ranges overlap there
+// may be more tiles than the grid, which counts on each row once, and the last are left out.
 __device__ __forceinline__ bool routed_tile(const I4Product &p, int size, int64_t index, int &expert, int64_t &first, int &rows) {
     const int lane = lane_id();
     // more tiles than a grid has, so that sums stay in 32 bits whatever the offsets say

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests.test_gpu_experts import (BF16, F16, F32, INF, bounded, check, check_route, loom, offsets_of,  # noqa: F401
-                                       operands, parts, product64)
+                                    operands, parts, product64)
 
 pytestmark = pytest.mark.gpu
 LOWEST = torch.finfo(F32).min
@@ -225,3 +225,27 @@ def test_large_sums(loom, device, tokens):  # noqa: F811
     got = loom.i4_matmul(loom.pack_int4(wq.to(device)), ws.to(device), loom.pack_int8(xq.to(device)), xs.to(device), group=group,
                          dtype=F32)
     assert torch.equal(got.cpu().double(), want)
+
+
+# ------------------------------------------------------------------ offsets that overlap
+
+@pytest.mark.parametrize("pairs,offsets", [(200, [0, 150, 0, 200]), (200, [0, 200, 0, 200, 0, 200, 190]), (7, [0, 7, 2, 6, 0, 7]),
+                                           (300, [200, 300, 0, 50, 20, 300]),
+                                           (300, [100, 200, 0, 50, 20, 40])])
+def test_overlapping_offsets(loom, device, pairs, offsets):  # noqa: F811
+    """Where ranges overlap, every element of a claimed row is as it was or one claimant's; no other row is written."""
+    experts, rows, k, group = len(offsets) - 1, 200, 64, 32
+    s = operands(experts, rows, k, pairs, group, F32, 3)
+    d = {n: t.to(device) for n, t in s.items()}
+    out = torch.full((pairs, rows), 7.0, device=device)
+    loom.i4_expert_matmul(loom.pack_int4(d["w"]), d["ws"], loom.pack_int8(d["x"]), d["xs"],
+                          torch.tensor(offsets, dtype=torch.int32, device=device), group=group, out=out)
+    out = out.cpu().double()
+    fits = out == 7.0
+    for e in range(experts):
+        a, b = offsets[e], offsets[e + 1]
+        if a < b:
+            y, size = product64(s["x"][a:b], s["w"][e], s["ws"][e], group)
+            v, tol = bounded(y, size, parts(k, group), s["xs"][a:b], None, F32)
+            fits[a:b] |= (out[a:b] - v).abs() <= tol
+    assert bool(fits.all())
