@@ -613,7 +613,11 @@ def _weights4(w, w_scale, group, lead, device, w_name, s_name):
     _require(group >= 1, "group must be positive")
     k = 8 * w.shape[-1]
     count = w.shape[0] * (w.shape[1] if lead == 3 else 1)
-    _buffer(w_scale, w_scale.dtype, count * -(-k // group), s_name, device)
+    groups = -(-k // group)
+    _buffer(w_scale, w_scale.dtype, count * groups, s_name, device)
+    # scales of shorter groups are more than enough, and would be read as if they were these
+    if w_scale.dim() > 1 and w_scale.shape[-1] != groups:
+        raise ValueError(f"{s_name} has {w_scale.shape[-1]} scales a channel, k {k} in groups of {group} needs {groups}")
     return k, kind
 
 

@@ -249,3 +249,19 @@ def test_overlapping_offsets(loom, device, pairs, offsets):  # noqa: F811
             v, tol = bounded(y, size, parts(k, group), s["xs"][a:b], None, F32)
             fits[a:b] |= (out[a:b] - v).abs() <= tol
     assert bool(fits.all())
+
+
+def test_scales_of_other_groups(loom, device):  # noqa: F811
+    """Scales made for another group length are refused; a longer flat buffer is read from its start."""
+    s = operands(2, 40, 256, 5, 32, F32, 1)
+    d = {n: t.to(device) for n, t in s.items()}
+    w, x, off = loom.pack_int4(d["w"]), loom.pack_int8(d["x"]), offsets_of([2, 3]).to(device)
+    for group in (64, 128, 256):
+        with pytest.raises(ValueError, match="scales a channel"):
+            loom.i4_matmul(w[0], d["ws"][0], x, group=group)
+        with pytest.raises(ValueError, match="scales a channel"):
+            loom.i4_expert_matmul(w, d["ws"], x, None, off, group=group)
+        with pytest.raises(ValueError, match="scales a channel"):
+            loom.i4_expert_gated_projection(w, d["ws"], w, d["ws"], x, None, off, group=group)
+    want = loom.i4_matmul(w[0], d["ws"][0], x, group=32)
+    assert torch.equal(loom.i4_matmul(w[0], d["ws"].flatten(), x, group=32), want)
