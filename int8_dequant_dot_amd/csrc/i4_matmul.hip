@@ -29,7 +29,7 @@ namespace {
 //
 // Memory bounds it: one token x 16384 x 8192 in groups of 128 takes 13.1 us (5.3 TB/s, of
 // it about 2.4 us a launch), the gated rows of 32 tokens x 8 routes over 128 experts of
-// 2048 x 4096 168 us (6.6 TB/s).  A workgroup of 16 rows took 14.8 and 250 us, three
+// 2048 x 4096 168 to 171 us (6.5 to 6.6 TB/s).  A workgroup of 16 rows took 14.8 and 250 us, three
 // records in flight 16.7 and 310, eight waves 18.7 and 257; 64-bit addresses instead of
 // offsets from the tile 13.7 and 222.
 template <int ST, int RI, int VG>

@@ -1,5 +1,5 @@
-// i4_tiles.hpp -- the tile of the 4-bit products: activations through LDS,
-// weights straight into registers, group sums on the int8 matrix cores.
+// i4_tiles.hpp -- the tile of the 4-bit products: activations, packed weights and
+// scales through LDS, group sums on the int8 matrix cores.
 #pragma once
 
 #include "i4_common.hpp"
@@ -34,11 +34,12 @@ __device__ __forceinline__ void gather_to_lds(const void *from, int at) {
 // weights, filled by direct loads; 16-byte piece c of row r sits at slot c ^ swizzle(r),
 // so that fragment reads meet no bank twice.
 //
-// What bounds it is the vector unit: each sum of 32 x 32 x 128 takes a conversion and a
-// multiply-add (256 of the 530 vector instructions of a wave's step of 256), its weights
-// three instructions for two registers.  4096 tokens x 8192 channels x k 28672 takes 1.05 ms
-// in groups of 128 (1840 TOP/s; without loads 0.88 to 0.93), 1.95 ms in groups of 32, four
-// times the conversions.  Not kept at that size: weights straight from memory to registers
+// The vector unit is the fuller one, 69 % of the cycles at 4096 tokens x 8192 channels x k
+// 28672, the matrix cores 41 %: each sum of 32 x 32 x 128 takes a conversion and a multiply-add
+// (256 of the 530 vector instructions of a wave's step of 256), its weights three instructions
+// for two registers; the rest is waits, of two waves a SIMD that meet at every step.  That size
+// takes 1.05 to 1.10 ms in groups of 128 (1750 to 1830 TOP/s; without loads 0.88 to 0.93), 1.95
+// in groups of 32, four times the conversions.  Not kept there: weights straight from memory to registers
 // (1.64 ms: a line for every 16 bytes of a lane), reads that wait for the barrier of their
 // own step (1.24 ms), scales read by each lane (1.21 ms), one wave a SIMD with twice the
 // tokens (1.22 ms: the sums go through the accumulation registers), 128 x 128 tiles, two a

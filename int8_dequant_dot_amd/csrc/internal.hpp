@@ -668,9 +668,12 @@ constexpr int64_t kI4MaxK = 131040, kI4MaxExperts = 1024;
 constexpr int i4_subs(int chunk_shift) { return chunk_shift >= 2 ? 1 : chunk_shift == 1 ? 2 : 4; }
 constexpr int kI4StreamWaves = 4, kI4StreamLoads = 8;
 // Token slots (4 or 8, a token takes subs of them) of the kernel for few tokens, 0: too
-// many tokens for it.  Of experts it takes those with up to 4 slots on average: with 6
-// rows each, 64 experts x 2048 x 2048 took 50 us so and 33 us in tiles, while at 28672 x
-// 8192, dense, 6 tokens took 26 us so and 38 us in tiles.
+// many tokens for it.  At 28672 x 8192, dense, 6 tokens took 26 us so and 38 us in tiles.
+// Of experts it takes those with up to 4 slots on average.  1 to 4 rows each in groups of
+// 128, so and in tiles: 64 experts x 2048 x 2048 gated 54 to 61 and 66 us, plain 38 to 42 and
+// 31 to 32; 8 x 14336 x 4096 gated 78 to 84 and 101 to 104, plain 52 to 55 and 56 to 60.  An
+// expert with more rows than slots has its weights read again: with 0 to 6 rows each, plain,
+// 64 experts take 45 and 30 us.  6 rows each, 50 and 33.
 constexpr int i4_stream_slots(int64_t tokens, int64_t experts, int subs) {
     if (tokens == 0) return 4;
     const int64_t each = experts > 0 ? ceil_of(tokens, tokens < experts ? tokens : experts) : tokens;

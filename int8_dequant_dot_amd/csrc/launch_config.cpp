@@ -210,8 +210,9 @@ int geo_group_routes(const int64_t *w, loom_launch_config *c) {
 
 // i4_matmul (rows, k, tokens, group), i4_expert_matmul and
 // i4_expert_gated_projection (rows, k, pairs, group, experts): one workgroup per
-// 32 tokens of one expert (at most: routed tiles that the offsets leave empty end
-// at once) and 32 channels a wave.
+// 1 to 8 tokens and 32 channels (gated 16) where weights stream, else per tile of
+// i4_tile_choice, 32 to 128 tokens of one expert and 32 to 256 channels.  Routed tiles
+// are counted as the offsets may need them at most; those that they do not need end at once.
 template <bool ROUTED, bool GATED>
 int geo_i4(const int64_t *w, loom_launch_config *c) {
     if (w[0] < 0 || w[1] < 0 || w[1] > kI4MaxK || w[2] < 0 || w[3] < 32) return LOOM_ERR_RANGE;

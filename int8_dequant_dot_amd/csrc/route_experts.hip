@@ -8,14 +8,19 @@
 // Ties go to the lower index.  Neighbouring choices may differ by less than a
 // step of f32, so wherever a choice is computed (and is not a logit itself) its
 // order is that of its 64-bit value: waves whose f32 choices lie apart by more
-// than their error are done with those, the few others compute them again in 64
-// bits.  Weights are f32.
+// than their error are done with those; where a sigmoid's do not, a few candidates are
+// put in the order of their 64-bit values, and where that is not enough, or the scores
+// are a softmax's, the wave computes every choice again in 64 bits.  Weights are f32.
 //
-// The vector unit bounds it: 65536 tokens x 256 experts in f32, the 8 best of 4 of 8
-// groups by sigmoid and bias, take 51 to 59 us, where their 71 MB would take 15; a wave
-// of four tokens runs 1.4 thousand instructions.  16 lanes hold a token where there are
-// many (fewer cross-lane steps a token), 64 where there are few.  With every choice in 64
-// bits the same took 190 us.
+// 65536 tokens x 256 experts in f32, the 8 best of 4 of 8 groups by sigmoid and bias, take
+// 49 to 59 us, where their 71 MB would take 15.  A wave of four tokens runs 1.3 thousand
+// vector instructions, 55 % of the cycles; it has 168 registers, so that three waves a SIMD
+// share the waits for chains of cross-lane steps, and 70 scalars that are kept in lanes.  16
+// lanes hold a token where there are many (fewer cross-lane steps a token), 64 where there
+// are few.  With every choice in 64 bits the same took 190 us.  By its bounds 1.2 % of its
+// waves order candidates and one in 8 thousand does all in 64 bits; with a softmax 0.9 % do
+// (57 us), and from top_k 13 on, where 16 lanes have no room for candidates, 2 to 2.5 %
+// (72 us, 78 at 16).
 // The gradient streams: 65536 x 256 bfloat16 logits through the softmax take 19 us (3.7 TB/s).
 #include <type_traits>
 
@@ -438,9 +443,9 @@ __device__ __forceinline__ int order_candidates(const RouteArgs &a, int64_t row,
     return id;
 }
 
-// The same choice from 64-bit values, for tokens whose f32 ones lie too close together.
-// A token in some hundreds needs it, so it takes few registers at a time, and a wave that
-// does takes about 7 us.  room: experts + groups values.
+// The same choice from 64-bit values, for waves whose f32 ones lie too close together.
+// Few need it, so it takes few registers at a time, and a wave that does takes about 7 us.
+// room: experts + groups values.
 template <int LOG, int R>
 __device__ __forceinline__ int choose_wide(const RouteArgs &a, int sub, float top, const float (&l)[R], const float (&bias)[R],
                                            double *room) {
